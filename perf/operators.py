@@ -50,7 +50,7 @@ def listed():
              min_p=0.0, tail=1.3),
         # a large batch, nucleus and min-p only: the kept sets are long
         dict(name="sample 128", op="sample", B=128, V=150_144, temperature=1.0, top_k=0,
-             top_p=0.9, min_p=1e-5, tail=0.7),
+             top_p=0.9, min_p=1e-5, tail=1.1),
         # a small vocabulary, odd sizes, mixed requests (greedy ones among them)
         dict(name="sample small", op="sample", B=7, V=5003, temperature=0.6, top_k=100, top_p=0.8,
              min_p=0.02, tail=1.0),
