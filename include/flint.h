@@ -78,7 +78,13 @@ enum {
  * build compiles the checks away.  Both export this same ABI. */
 
 /* Workspace kinds for flint_workspace_bytes. */
-enum { FLINT_OP_ROUTE = 0, FLINT_OP_DECODE = 1, FLINT_OP_PREFILL = 2, FLINT_OP_GEMV = 3 };
+enum {
+  FLINT_OP_ROUTE = 0,
+  FLINT_OP_DECODE = 1,
+  FLINT_OP_PREFILL = 2,
+  FLINT_OP_GEMV = 3,
+  FLINT_OP_APPEND = 4
+};
 
 /*
  * One MoE layer's weights (all device pointers, read only).
@@ -158,10 +164,13 @@ FLINT_API const char *flint_last_cuda_error(void);
 FLINT_API const char *flint_strerror(int code);
 
 /* Bytes of workspace `op` needs for n rows (B for decode and gemv, T for
- * route and prefill); for FLINT_OP_GEMV, n = B and the size also depends on
- * N via flint_gemv_workspace_bytes.  Returns 0 for an unsupported n. */
+ * route, prefill and append); for FLINT_OP_GEMV, n = B and the size also
+ * depends on N via flint_gemv_workspace_bytes; flint_attn_decode's depends on
+ * its heads via flint_attn_workspace_bytes.  Returns 0 for an unsupported n
+ * (or heads). */
 FLINT_API size_t flint_workspace_bytes(int op, int n);
 FLINT_API size_t flint_gemv_workspace_bytes(int N, int B);
+FLINT_API size_t flint_attn_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim);
 
 /* Zero a whole workspace (async on `stream`), counters and status word
  * included. */
@@ -407,6 +416,161 @@ FLINT_API int flint_int4_gemv_noalloc(const uint8_t *q, const uint16_t *s, int N
  * flint_int4_gemv_noalloc call clears the word.  Allocates nothing.
  */
 FLINT_API int flint_int4_gemv_noalloc_status(int *status, void *stream);
+
+/* ---------------------------------------------------------------- the cache
+ * The attention between two MoE blocks: a paged cache of keys and values, the
+ * append that fills it and the decode attention that reads it.  Flint's
+ * layers have 32 query heads over 4 KV heads of 128 with an RMSNorm on each
+ * head of q and k, rotary positions (theta 10,000) with a window of 513 keys
+ * in the sliding layers and neither in the 14 full ones, and a learned sink
+ * per head ("How to Run Flint Locally", sections "The architecture, from
+ * config.json" and "Attention sinks"; TandemLLM "21 Flint", section 21.1).
+ * The calls take these as arguments.
+ *
+ * flint_kv_cache describes one layer's pages (a host struct, read during the
+ * call only).  Element (page p, KV head h, row r, element i) of K is at
+ * k[p * page_stride + h * head_stride + r * token_stride + i], of V likewise:
+ * [page][head][row][dim] and [page][row][head][dim] pages, K and V in one
+ * allocation or several layers in one are all strides.
+ *   k, v      device pointers, 16-byte aligned
+ *   type      FLINT_KV_BF16, or FLINT_KV_E4M3: FP8 E4M3 codes, one byte each,
+ *             value = code * scale of its KV head
+ *   num_pages 1 .. 2^31 - 1; page_size rows a page, a multiple of 16, at most
+ *             4,096; heads 1 .. 256; head_dim 64 or 128
+ *   *_stride  in elements, at least 1 row each, each a multiple of 16 bytes;
+ *             heads and rows of a page may not overlap
+ *   k_scale, v_scale  fp32 [heads] device arrays for FLINT_KV_E4M3 (NULL:
+ *             all 1), positive and finite; not read for FLINT_KV_BF16
+ */
+#define FLINT_KV_BF16 0
+#define FLINT_KV_E4M3 1
+#define FLINT_MAX_PAGE 4096
+#define FLINT_MAX_APPEND_T (1 << 20)
+#define FLINT_MAX_ATTN_B 4096
+#define FLINT_MAX_ATTN_GROUP 16
+#define FLINT_MAX_VOCAB (1 << 18)
+typedef struct {
+  void *k;
+  void *v;
+  int type;
+  int num_pages;
+  int page_size;
+  int heads;
+  int head_dim;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t token_stride;
+  const float *k_scale;
+  const float *v_scale;
+} flint_kv_cache;
+
+/*
+ * Append T tokens' keys and values to the cache, with each head's RMSNorm and
+ * the rotary positions applied on the way, and the same for the queries:
+ *   x' = x * rsqrt(mean(x^2) + FLINT_RMS_EPS) * norm      (q and k; norm NULL: x' = x)
+ *   pair (a, b) number i of the first rope_dim elements, t = pos * theta^(-2i / rope_dim):
+ *     (a cos t - b sin t, b cos t + a sin t)              (q and k; rope_dim 0: none)
+ *     pairs (i, i + rope_dim / 2), or (2i, 2i + 1) with interleaved != 0
+ *   K[slot] = the rotated k, V[slot] = v, rounded to the cache's type once
+ *     (E4M3: value / scale, saturating at +-448)
+ * in fp32 from the bf16 inputs, the angle reduced to a turn in fp64.
+ *   q       bf16, token t's q_heads * head_dim elements at q + t * q_stride;
+ *           NULL with q_heads = 0: no queries.  k, v: heads * head_dim
+ *           elements a token, likewise.  Strides in elements, multiples of 8
+ *           (the rows of one fused projection are fine)
+ *   slots   int64 [T]: slot = page * page_size + row.  A negative slot marks
+ *           a padding token: nothing of it is written, its q_out row neither.
+ *           A slot past the last page records FLINT_EDEVICE and its token is
+ *           skipped the same way.  The slots of one call are distinct: of two
+ *           tokens with the same slot, which one's 16-byte pieces a row ends
+ *           up with is not defined
+ *   pos     int32 [T], >= 0
+ *   rope_dim 0, or a multiple of 16 up to head_dim; theta > 0, finite
+ *   q_norm, k_norm  bf16 [head_dim] or NULL
+ *   q_out   bf16, token t's row at q_out + t * q_out_stride; may be q itself
+ *           (same stride), and may not overlap it otherwise
+ *   ws      workspace of flint_workspace_bytes(FLINT_OP_APPEND, T) (its
+ *           status word); 1 <= T <= FLINT_MAX_APPEND_T
+ */
+FLINT_API int flint_kv_append(const flint_kv_cache *cache, const uint16_t *q, int64_t q_stride,
+                              const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                              int64_t v_stride, int T, int q_heads, const int64_t *slots,
+                              const int32_t *pos, int rope_dim, int interleaved, double theta,
+                              const uint16_t *q_norm, const uint16_t *k_norm, uint16_t *q_out,
+                              int64_t q_out_stride, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Decode attention: one query token for each of B sequences, over a prefix of
+ * prefix_len keys that all of them share (computed once for the batch: each
+ * of its rows is read once, not once a sequence) and the lens[b] keys of
+ * their own behind it.  The cache holds the query token's own key already
+ * (flint_kv_append), so sequence b's query stands at prefix_len + lens[b] - 1:
+ *   s_j = scale * (q . K_j), j over the sequence's prefix_len + lens[b] keys,
+ *         with window > 0 the last `window` of them only
+ *   out = sum_j exp(s_j) V_j / (sum_j exp(s_j) + exp(sinks[head]))
+ *   lse = log of that denominator
+ * (without sinks: without that term), query head h reading KV head
+ * h / (q_heads / heads).  A row without any key gives out = 0 and lse = its
+ * sink (or -inf).  Masked rows of the cache (behind a sequence's last key,
+ * before its window, other pages) are never read into a result: they may
+ * hold NaN.
+ *   q       bf16, sequence b's q_heads * head_dim elements at q + b * q_stride
+ *           (stride a multiple of 8); out bf16 likewise; out may be q (same
+ *           stride)
+ *   q_heads a multiple of the cache's heads, at most FLINT_MAX_ATTN_GROUP
+ *           times as many; 1 <= B <= FLINT_MAX_ATTN_B
+ *   page_table  int32 [B][max_pages]: the pages of each sequence's own keys in
+ *           order; entries past its last page are not read
+ *   lens    int32 [B]; lens[b] < 0 marks a padding row: it has no keys at all,
+ *           the prefix's neither (out = 0).  lens[b] above max_pages *
+ *           page_size records FLINT_EDEVICE and is cut to that
+ *   prefix_pages  int32 [ceil(prefix_len / page_size)] (NULL with prefix_len
+ *           = 0); prefix_len >= 0.  prefix_len + max_pages * page_size <= 2^30
+ *   window  0: none
+ *   sinks   fp32 [q_heads] or NULL;  lse fp32 [B][q_heads] or NULL
+ *   ws      workspace of flint_attn_workspace_bytes(B, q_heads, heads,
+ *           head_dim)
+ * A page number outside the cache records FLINT_EDEVICE; its keys count as
+ * zeros.  fp32 scores, softmax statistics and sums; the weights exp(s_j - m)
+ * enter the second product in 16 bits (see the kernels).  The result does not
+ * depend on the other sequences' contents, but its last bits may depend on
+ * how the call's keys are split, which follows the lengths.
+ */
+FLINT_API int flint_attn_decode(const flint_kv_cache *cache, const uint16_t *q, int64_t q_stride,
+                                int B, int q_heads, const int32_t *page_table, int max_pages,
+                                const int32_t *lens, const int32_t *prefix_pages, int prefix_len,
+                                float scale, int window, const float *sinks, uint16_t *out,
+                                int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/*
+ * Sample one token a row from the head's logits with given random numbers
+ * (the guide's settings for Flint are temperature 1, top-p 0.95, top-k 20).
+ * For row b over its V logits z, with order = larger logit first, equal
+ * logits by the lower index:
+ *   p_i = exp((z_i - max z) / temperature[b])
+ *   top-k: the first top_k[b] tokens of the order
+ *   top-p: of those, the shortest prefix of the order whose mass is at least
+ *          top_p[b] of theirs (one token at least)
+ *   min-p: of those, the tokens with p_i >= min_p[b] (the first one always)
+ *   token[b]   = the lowest index i with sum_{kept j <= i} p_j > u[b] * sum_{kept} p_j
+ *   logprob[b] = log(p_token / sum_{kept} p_j)
+ *   logits  fp32, row b at logits + b * stride (stride >= V elements)
+ *   temperature, top_p, min_p, u  fp32 [B], top_k int32 [B]; NULL: 1, off,
+ *           off, and for top_k off; u may not be NULL.  temperature not above
+ *           0 (NaN too): greedy, the first token of the order (logprob 0).
+ *           Off: top_k <= 0 or >= V, top_p >= 1 or NaN, min_p <= 0 or NaN.
+ *           u in [0, 1) (below: as 0; at or above 1: the last kept token)
+ *   A NaN logit is never chosen; tokens at +inf share all of the mass.  A row
+ *   whose logits are all -inf or NaN gives token -1 and logprob -inf.
+ *   token int32 [B]; logprob fp32 [B] or NULL; 1 <= B <= 65,535,
+ *   1 <= V <= FLINT_MAX_VOCAB.  Needs no workspace.
+ * The result is a function of the row alone: the same for every run and batch.
+ */
+FLINT_API int flint_sample(const float *logits, int64_t stride, int B, int V,
+                           const float *temperature, const int32_t *top_k, const float *top_p,
+                           const float *min_p, const float *u, int32_t *token, float *logprob,
+                           void *stream);
 
 #ifdef __cplusplus
 }

@@ -19,7 +19,9 @@ LIB_PATH = os.path.join(HERE, "libflint.so")
 DEBUG_LIB_PATH = os.path.join(HERE, "libflint_debug.so")
 
 FLINT_OK, FLINT_EINVAL, FLINT_ECUDA, FLINT_ETIMEOUT, FLINT_EDEVICE = range(5)
-FLINT_OP_ROUTE, FLINT_OP_DECODE, FLINT_OP_PREFILL, FLINT_OP_GEMV = range(4)
+FLINT_OP_ROUTE, FLINT_OP_DECODE, FLINT_OP_PREFILL, FLINT_OP_GEMV, FLINT_OP_APPEND = range(5)
+FLINT_KV_BF16, FLINT_KV_E4M3 = range(2)
+MAX_APPEND_T, MAX_ATTN_B, MAX_ATTN_GROUP, MAX_VOCAB = 1 << 20, 4096, 16, 1 << 18
 HIDDEN, EXPERTS, TOP_K, EXPERT_I, SHARED_I, GROUP, MAX_DECODE_B = 2048, 256, 6, 512, 1024, 128, 8
 
 EXPORTS = ("flint_version", "flint_strerror", "flint_last_cuda_error", "flint_workspace_bytes",
@@ -29,8 +31,19 @@ EXPORTS = ("flint_version", "flint_strerror", "flint_last_cuda_error", "flint_wo
            "flint_moe_prefill", "flint_int4_gemv", "flint_int4_gemv_affine", "flint_int4_gemv_nvfp4",
            "flint_int4_gemv_noalloc",
            "flint_int4_gemv_noalloc_status",
+           "flint_attn_workspace_bytes", "flint_kv_append", "flint_attn_decode", "flint_sample",
            "flint_debug_set_wait_polls", "flint_debug_prefill_events",
            "flint_debug_prefill_stage_ms")
+
+
+
+class flint_kv_cache(C.Structure):
+    """One layer's pages (make_kv_cache)."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("type", C.c_int), ("num_pages", C.c_int),
+                ("page_size", C.c_int), ("heads", C.c_int), ("head_dim", C.c_int),
+                ("page_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("token_stride", C.c_int64), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
 
 _lib = None
 _loaded = {}  # path -> CDLL with its signatures set
@@ -118,6 +131,14 @@ def _load(path: str) -> C.CDLL:
         L.flint_int4_gemv_nvfp4.argtypes = [vp, vp, C.c_float, i, i, vp, i, vp, vp, vp, sz, vp]
         L.flint_int4_gemv_noalloc.argtypes = [vp, vp, i, i, vp, i, vp, vp, vp]
         L.flint_int4_gemv_noalloc_status.argtypes = [C.POINTER(C.c_int), vp]
+        i64, kp = C.c_int64, C.POINTER(flint_kv_cache)
+        L.flint_attn_workspace_bytes.restype = sz
+        L.flint_attn_workspace_bytes.argtypes = [i, i, i, i]
+        L.flint_kv_append.argtypes = [kp, vp, i64, vp, i64, vp, i64, i, i, vp, vp, i, i,
+                                      C.c_double, vp, vp, vp, i64, vp, sz, vp]
+        L.flint_attn_decode.argtypes = [kp, vp, i64, i, i, vp, i, vp, vp, i, C.c_float, i, vp, vp,
+                                        i64, vp, vp, sz, vp]
+        L.flint_sample.argtypes = [vp, i64, i, i, vp, vp, vp, vp, vp, vp, vp, vp]
         for name in EXPORTS:
             getattr(L, name).restype = getattr(L, name).restype or i
         _loaded[path] = L
@@ -296,3 +317,78 @@ def flint_int4_gemv_noalloc_status(stream=None) -> int:
     _check(lib().flint_int4_gemv_noalloc_status(C.byref(st), _stream(stream)),
            "flint_int4_gemv_noalloc_status")
     return st.value
+
+
+# ------------------------------------------------- the cache, its attention, sampling
+def _local(where: str, *tensors):
+    """Refuse tensors that are not on the current CUDA device: the call
+    launches there, and ``stream`` is one of its streams."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            if dev is None:
+                dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+            if t.get_device() != dev or dev < 0:
+                raise FlintError(FLINT_EINVAL, where)
+
+
+def make_kv_cache(k, v, k_scale=None, v_scale=None) -> flint_kv_cache:
+    """The C cache struct from K and V page tensors [pages, heads, page_size,
+    head_dim], bf16 (or its 16-bit patterns as int16) or float8_e4m3fn (or
+    uint8), and for the 8-bit cache the fp32 [heads] scales.  Any strides that
+    flint.h takes: a [pages, page_size, heads, head_dim] cache is passed as
+    ``k.transpose(1, 2)``.  The struct keeps a reference to the tensors."""
+    if (k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or
+            k.element_size() > 2 or (k.shape[3] > 1 and k.stride(3) != 1)):
+        raise ValueError("make_kv_cache: K and V pages [pages, heads, page_size, head_dim] of one "
+                         "layout and one 16- or 8-bit type, head_dim contiguous")
+    for s in (k_scale, v_scale):
+        if s is not None and (s.numel() != k.shape[1] or not s.is_contiguous() or
+                              s.element_size() != 4):
+            raise ValueError("make_kv_cache: scales are contiguous fp32 [heads]")
+    _local("make_kv_cache", k, v, k_scale, v_scale)
+    pages, heads, page, dim = k.shape
+    cache = flint_kv_cache(_ptr(k), _ptr(v), FLINT_KV_BF16 if k.element_size() == 2 else
+                           FLINT_KV_E4M3, pages, page, heads, dim, k.stride(0), k.stride(1),
+                           k.stride(2), _ptr(k_scale), _ptr(v_scale))
+    cache._tensors = (k, v, k_scale, v_scale)
+    return cache
+
+
+def flint_attn_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return lib().flint_attn_workspace_bytes(B, q_heads, kv_heads, head_dim)
+
+
+def flint_kv_append(cache: flint_kv_cache, q, q_stride: int, k, k_stride: int, v, v_stride: int,
+                    T: int, q_heads: int, slots, pos, rope_dim: int, interleaved: bool,
+                    theta: float, q_norm, k_norm, q_out, q_out_stride: int, ws, ws_bytes: int,
+                    stream=None):
+    """``cache``: from ``make_kv_cache``."""
+    _local("flint_kv_append", q, k, v, slots, pos, q_norm, k_norm, q_out, ws)
+    _check(lib().flint_kv_append(C.byref(cache), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
+                                 v_stride, T, q_heads, _ptr(slots), _ptr(pos), rope_dim,
+                                 1 if interleaved else 0, theta, _ptr(q_norm), _ptr(k_norm),
+                                 _ptr(q_out), q_out_stride, _ptr(ws), ws_bytes, _stream(stream)),
+           "flint_kv_append")
+
+
+def flint_attn_decode(cache: flint_kv_cache, q, q_stride: int, B: int, q_heads: int, page_table,
+                      max_pages: int, lens, prefix_pages, prefix_len: int, scale: float,
+                      window: int, sinks, out, out_stride: int, lse, ws, ws_bytes: int,
+                      stream=None):
+    """``cache``: from ``make_kv_cache``."""
+    _local("flint_attn_decode", q, page_table, lens, prefix_pages, sinks, out, lse, ws)
+    _check(lib().flint_attn_decode(C.byref(cache), _ptr(q), q_stride, B, q_heads,
+                                   _ptr(page_table), max_pages, _ptr(lens), _ptr(prefix_pages),
+                                   prefix_len, scale, window, _ptr(sinks), _ptr(out), out_stride,
+                                   _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)),
+           "flint_attn_decode")
+
+
+def flint_sample(logits, stride: int, B: int, V: int, temperature, top_k, top_p, min_p, u, token,
+                 logprob, stream=None):
+    _local("flint_sample", logits, temperature, top_k, top_p, min_p, u, token, logprob)
+    _check(lib().flint_sample(_ptr(logits), stride, B, V, _ptr(temperature), _ptr(top_k),
+                              _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(logprob),
+                              _stream(stream)), "flint_sample")

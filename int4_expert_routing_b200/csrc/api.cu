@@ -44,6 +44,42 @@ bool decode_batch_ok(const flint_moe_layer *l, int B) {
                                                          : FLINT_MAX_DECODE_B);
 }
 
+bool head_dim_ok(int d) { return d == 64 || d == 128; }
+bool heads_ok(int q_heads, int kv_heads) {
+  return kv_heads >= 1 && kv_heads <= 256 && q_heads >= kv_heads && q_heads % kv_heads == 0 &&
+         q_heads / kv_heads <= FLINT_MAX_ATTN_GROUP;
+}
+
+// A layer's pages: strides of at least a row, whole 16-byte pieces, below the
+// 2^40 bytes a tensor map takes, and no two elements at one address for the
+// two layouts a page can have (rows inside heads or heads inside rows).
+bool cache_ok(const flint_kv_cache *c) {
+  if (!c || !aligned16(c->k) || !aligned16(c->v) ||
+      (c->type != FLINT_KV_BF16 && c->type != FLINT_KV_E4M3) || c->num_pages < 1 ||
+      c->page_size < 16 || c->page_size > FLINT_MAX_PAGE || c->page_size % 16 || c->heads < 1 ||
+      c->heads > 256 || !head_dim_ok(c->head_dim))
+    return false;
+  if (c->type == FLINT_KV_E4M3 &&
+      ((c->k_scale && !aligned4(c->k_scale)) || (c->v_scale && !aligned4(c->v_scale))))
+    return false;
+  const int64_t elt = c->type == FLINT_KV_BF16 ? 2 : 1, most = ((int64_t)1 << 39) / elt;
+  auto stride_ok = [&](int64_t s, int64_t n) {
+    return n <= 1 || (s >= c->head_dim && s <= most && (s * elt) % 16 == 0);
+  };
+  if (!stride_ok(c->token_stride, c->page_size) || !stride_ok(c->head_stride, c->heads) ||
+      !stride_ok(c->page_stride, c->num_pages))
+    return false;
+  const int64_t row = (c->page_size - 1) * c->token_stride + c->head_dim;
+  const int64_t head = c->heads > 1 ? (c->heads - 1) * c->head_stride + c->head_dim : c->head_dim;
+  if (c->heads > 1 && c->head_stride < row && c->token_stride < head) return false;
+  return true;
+}
+
+// rows of `n` bf16 elements, `stride` apart, in 16-byte pieces
+bool rows_ok(const void *p, int64_t stride, int64_t n) {
+  return aligned16(p) && stride >= n && stride % 8 == 0 && stride <= ((int64_t)1 << 40);
+}
+
 thread_local cudaError_t g_last_cuda = cudaSuccess;
 thread_local const char *g_last_where = "";
 thread_local const char *g_step = "";
@@ -100,6 +136,8 @@ size_t flint_workspace_bytes(int op, int n) {
       return n <= FLINT_MAX_PREFILL_T ? prefill_layout(n).total : 0;
     case FLINT_OP_GEMV:
       return 0;  // depends on N: flint_gemv_workspace_bytes
+    case FLINT_OP_APPEND:
+      return n <= FLINT_MAX_APPEND_T ? 256 : 0;
     default:
       return 0;
   }
@@ -108,6 +146,12 @@ size_t flint_workspace_bytes(int op, int n) {
 size_t flint_gemv_workspace_bytes(int N, int B) {
   if (N < 1 || B < 1 || B > FLINT_MAX_DECODE_B) return 0;
   return gemv_ws_bytes(N, B);
+}
+
+size_t flint_attn_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim) {
+  if (B < 1 || B > FLINT_MAX_ATTN_B || !heads_ok(q_heads, kv_heads) || !head_dim_ok(head_dim))
+    return 0;
+  return attn_ws_bytes(B, q_heads, kv_heads, head_dim);
 }
 
 int flint_workspace_init(void *ws, size_t ws_bytes, void *stream) {
@@ -267,6 +311,68 @@ int flint_moe_prefill(const flint_moe_layer *layer, const uint16_t *x, int T, ui
     return FLINT_EINVAL;
   return from_cuda(launch_prefill(layer_args(layer), x, T, out, static_cast<char *>(ws),
                                   static_cast<cudaStream_t>(stream)));
+}
+
+int flint_kv_append(const flint_kv_cache *cache, const uint16_t *q, int64_t q_stride,
+                    const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride, int T,
+                    int q_heads, const int64_t *slots, const int32_t *pos, int rope_dim,
+                    int interleaved, double theta, const uint16_t *q_norm, const uint16_t *k_norm,
+                    uint16_t *q_out, int64_t q_out_stride, void *ws, size_t ws_bytes,
+                    void *stream) {
+  if (!cache_ok(cache) || T < 1 || T > FLINT_MAX_APPEND_T) return FLINT_EINVAL;
+  const int64_t d = cache->head_dim, n = cache->heads * d;
+  if (!rows_ok(k, k_stride, n) || !rows_ok(v, v_stride, n) || !slots || !pos ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u) || !aligned4(pos) || rope_dim < 0 ||
+      rope_dim % 16 || rope_dim > d || !(theta > 0.0) || theta > 1e300 ||
+      (q_norm && !aligned16(q_norm)) || (k_norm && !aligned16(k_norm)) || !aligned16(ws) ||
+      ws_bytes < flint_workspace_bytes(FLINT_OP_APPEND, T))
+    return FLINT_EINVAL;
+  if (!q) {
+    if (q_heads != 0) return FLINT_EINVAL;
+  } else if (!heads_ok(q_heads, cache->heads) || !rows_ok(q, q_stride, q_heads * d) ||
+             !rows_ok(q_out, q_out_stride, q_heads * d) || (q_out == q && q_out_stride != q_stride)) {
+    return FLINT_EINVAL;
+  }
+  const AppendArgs a{q, k, v, q_stride, k_stride, v_stride, T, q_heads, slots, pos, rope_dim,
+                     interleaved != 0, q_norm, k_norm, q_out, q_out_stride, cache->k, cache->v,
+                     cache->type, cache->num_pages, cache->page_size, cache->heads,
+                     cache->head_dim, cache->page_stride, cache->head_stride,
+                     cache->token_stride, cache->k_scale, cache->v_scale,
+                     reinterpret_cast<uint32_t *>(ws) + 1};
+  return from_cuda(launch_append(a, theta, static_cast<cudaStream_t>(stream)));
+}
+
+int flint_attn_decode(const flint_kv_cache *cache, const uint16_t *q, int64_t q_stride, int B,
+                      int q_heads, const int32_t *page_table, int max_pages, const int32_t *lens,
+                      const int32_t *prefix_pages, int prefix_len, float scale, int window,
+                      const float *sinks, uint16_t *out, int64_t out_stride, float *lse, void *ws,
+                      size_t ws_bytes, void *stream) {
+  if (!cache_ok(cache) || B < 1 || B > FLINT_MAX_ATTN_B || !heads_ok(q_heads, cache->heads))
+    return FLINT_EINVAL;
+  const int64_t n = (int64_t)q_heads * cache->head_dim;
+  if (!rows_ok(q, q_stride, n) || !rows_ok(out, out_stride, n) ||
+      (out == q && out_stride != q_stride) || !aligned4(page_table) || max_pages < 1 ||
+      !aligned4(lens) || prefix_len < 0 || (prefix_len > 0 && !aligned4(prefix_pages)) ||
+      (int64_t)max_pages * cache->page_size + prefix_len > ((int64_t)1 << 30) ||
+      !(scale == scale) || window < 0 || (sinks && !aligned4(sinks)) || (lse && !aligned4(lse)) ||
+      !aligned16(ws) ||
+      ws_bytes < flint_attn_workspace_bytes(B, q_heads, cache->heads, cache->head_dim))
+    return FLINT_EINVAL;
+  const AttnArgs a{*cache, q, q_stride, B, q_heads, page_table, max_pages, lens, prefix_pages,
+                   prefix_len, scale, window, sinks, out, out_stride, lse};
+  return from_cuda(launch_attn(a, static_cast<char *>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+int flint_sample(const float *logits, int64_t stride, int B, int V, const float *temperature,
+                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                 int32_t *token, float *logprob, void *stream) {
+  if (!aligned16(logits) || B < 1 || B > 65535 || V < 1 || V > FLINT_MAX_VOCAB || stride < V ||
+      stride > ((int64_t)1 << 40) || (temperature && !aligned4(temperature)) ||
+      (top_k && !aligned4(top_k)) || (top_p && !aligned4(top_p)) || (min_p && !aligned4(min_p)) ||
+      !aligned4(u) || !aligned4(token) || (logprob && !aligned4(logprob)))
+    return FLINT_EINVAL;
+  const SampleArgs a{logits, stride, B, V, temperature, top_k, top_p, min_p, u, token, logprob};
+  return from_cuda(launch_sample(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,894 @@
+// Decode attention over the paged cache (flint_attn_decode): one query token a
+// sequence, a prefix that all sequences share and keys of their own.
+//
+// Rows and units.  Query row R = b * G + g of KV head h is query head
+// h * G + g of sequence b (G query heads share a KV head).  A unit is a block
+// of rows of one KV head over one run of 64-key tiles:
+//   - an own unit (b, h): the G rows of one sequence over the keys of its own
+//     that its window leaves, and, with a window, over the part of the prefix
+//     that it leaves.  (With a window the rows of a batch see different parts
+//     of the prefix, so each reads its own; at most `window` keys, from L2.)
+//   - a prefix unit (block, h), without a window: rows of many sequences over
+//     the whole prefix, so that a key is read once for all of them.
+// The tiles of all units form one list, which the CTAs of a persistent kernel
+// share evenly: CTA c takes tiles [c n / N, (c + 1) n / N), whatever the
+// sequences' lengths.  A unit that falls to several CTAs is summed from their
+// parts by k_attn_combine; part (unit u, CTA c) is written to slot u + c,
+// which no two parts share since the list advances in u or c at each part.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace flint {
+
+constexpr int kAtKeys = 64;       // keys of a tile
+constexpr int kAtWarps = 4;       // consumer warps, 16 keys of each tile each
+constexpr int kAtThreads = 32 * (kAtWarps + 1);
+constexpr int kAtMaxCtas = 512;
+constexpr int kAtPrefixRows = 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+FLINT_DEV float at_ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------ the plan
+struct AttnK {
+  const uint16_t *q;
+  int64_t q_stride;
+  int B, G, H;               // sequences, query heads a KV head, KV heads
+  const int32_t *table;
+  int max_pages;
+  const int32_t *lens, *prefix_pages;
+  int prefix_len, window;
+  int page_size, num_pages, box_rows;
+  float scale2;              // scale * log2(e)
+  const float *k_scale, *v_scale, *sinks;
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;
+  uint32_t *status;
+  int32_t *cum;              // [B + 1] running tiles of the sequences (one KV head)
+  float *o_own, *o_pre;      // parts: [slot][rows][D], and their (max, sum)
+  float2 *ml_own, *ml_pre;
+  int ctas_pre;              // CTAs of the prefix list
+  int pre_rows;              // rows of a prefix unit
+};
+
+// The part of the keys that sequence b's row sees, as 64-key tiles.
+struct Span {
+  int n;             // own keys
+  int p_lo, o_lo;    // first visible prefix key (window only) and own key
+  int p_tiles, o_tiles;
+};
+FLINT_DEV Span seq_span(const AttnK &a, int b) {
+  Span s;
+  int n = a.lens[b];
+  const int most = a.max_pages * a.page_size;
+  if (n > most) {
+    set_status(a.status, kStatusDevice);
+    n = most;
+  }
+  s.n = n;
+  s.p_lo = a.prefix_len;
+  s.o_lo = 0;
+  s.p_tiles = 0;
+  if (n < 0) {
+    s.n = 0, s.o_tiles = 0;
+    return s;
+  }
+  if (a.window > 0) {
+    s.o_lo = max(0, n - a.window);
+    if (n < a.window) {
+      s.p_lo = max(0, a.prefix_len - (a.window - n));
+      if (s.p_lo < a.prefix_len)
+        s.p_tiles = ceil_div(a.prefix_len, kAtKeys) - s.p_lo / kAtKeys;
+    }
+  }
+  s.o_tiles = n > 0 ? ceil_div(n, kAtKeys) - s.o_lo / kAtKeys : 0;
+  return s;
+}
+FLINT_DEV int list_ctas(long long tiles, int grid) {
+  return (int)(tiles < grid ? (tiles > 0 ? tiles : 1) : grid);
+}
+FLINT_DEV long long list_start(long long tiles, int ctas, int c) { return tiles * c / ctas; }
+// the CTA that holds tile t
+FLINT_DEV int list_cta(long long tiles, int ctas, long long t) {
+  int c = (int)(t * ctas / tiles);
+  while (c + 1 < ctas && list_start(tiles, ctas, c + 1) <= t) ++c;
+  while (c > 0 && list_start(tiles, ctas, c) > t) --c;
+  return c;
+}
+
+// ------------------------------------------------------------------ matrix pieces
+FLINT_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FLINT_DEV void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FLINT_DEV uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+FLINT_DEV void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// two E4M3 codes (low and high byte of v) as fp16, exact
+FLINT_DEV uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  uint32_t d;
+  asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(v));
+  return d;
+}
+FLINT_DEV uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+FLINT_DEV uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+FLINT_DEV void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
+                           uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// ------------------------------------------------------------------ parts kernel
+// Shared-memory tile of kAtKeys rows of D elements: row bytes 256 (two halves
+// of 128), 128 or 64, in the TMA's 128- (64-) byte swizzle.
+template <int kD, bool kF8>
+struct AtTile {
+  static constexpr int kRow = kD * (kF8 ? 1 : 2);
+  static constexpr int kHalfRow = kRow > 128 ? 128 : kRow;  // bytes of a box's row
+  static constexpr int kHalves = kRow / kHalfRow;
+  static constexpr int kHalfBytes = kHalfRow * kAtKeys;
+  static constexpr int kBytes = kRow * kAtKeys;
+  static constexpr int kStages = kBytes >= 16384 ? 3 : (kBytes >= 8192 ? 6 : 10);
+  // byte offset of 16-byte chunk c of row r
+  static FLINT_DEV uint32_t at(int r, int c) {
+    if (kHalfRow == 128)
+      return (uint32_t)((c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  }
+};
+
+struct AtTileDesc {
+  bool prefix;   // pages of the prefix, else of sequence b
+  int b, h;      // sequence (own pages), KV head
+  int key0;      // first key of the tile
+  int lo, hi;    // visible keys [lo, hi)
+};
+
+// Walks this CTA's tiles.  kPre: prefix units of kRows rows; else own units.
+template <bool kPre>
+struct AtWalk {
+  const AttnK &a;
+  const int32_t *cum;  // shared memory copy (own)
+  long long t, end;
+  int b, h, unit;      // current unit (prefix: b = row block)
+  int in, n;           // tile in the unit, its tiles
+  Span s;
+  FLINT_DEV AtWalk(const AttnK &a_, const int32_t *cum_) : a(a_), cum(cum_) {}
+  FLINT_DEV void seek(long long t0, long long t1) {
+    t = t0, end = t1;
+    if (t >= end) return;
+    if (kPre) {
+      n = ceil_div(a.prefix_len, kAtKeys);
+      unit = (int)(t / n);
+      in = (int)(t - (long long)unit * n);
+      b = unit / a.H, h = unit % a.H;
+    } else {
+      int lo = 0, hi = a.B;  // the last b with H cum[b] <= t, its unit not empty
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if ((long long)a.H * cum[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      n = cum[b + 1] - cum[b];
+      const long long r = t - (long long)a.H * cum[b];
+      h = (int)(r / n);
+      in = (int)(r - (long long)h * n);
+      unit = b * a.H + h;
+      s = seq_span(a, b);
+    }
+  }
+  FLINT_DEV bool done() const { return t >= end; }
+  FLINT_DEV AtTileDesc tile() const {
+    AtTileDesc d;
+    d.b = b, d.h = h;
+    if (kPre) {
+      d.prefix = true, d.key0 = in * kAtKeys, d.lo = 0, d.hi = a.prefix_len;
+    } else if (in < s.p_tiles) {
+      d.prefix = true, d.key0 = (s.p_lo / kAtKeys + in) * kAtKeys, d.lo = s.p_lo;
+      d.hi = a.prefix_len;
+    } else {
+      d.prefix = false, d.key0 = (s.o_lo / kAtKeys + in - s.p_tiles) * kAtKeys, d.lo = s.o_lo;
+      d.hi = s.n;
+    }
+    return d;
+  }
+  // to the next tile; true if it begins another unit (or the list ends)
+  FLINT_DEV bool next() {
+    ++t, ++in;
+    if (t >= end) return true;
+    if (in < n) return false;
+    in = 0;
+    ++unit;
+    if (++h == a.H) {
+      h = 0, ++b;
+      if (!kPre) {
+        while (cum[b + 1] == cum[b]) ++b, unit += a.H;
+        n = cum[b + 1] - cum[b];
+        s = seq_span(a, b);
+      }
+    }
+    return true;
+  }
+};
+
+// kRows = 8 kNT query rows a unit
+template <int kD, bool kF8, int kNT, bool kPre>
+__global__ void __launch_bounds__(kAtThreads, kNT <= 2 ? 2 : 1)
+    k_attn_parts(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const __grid_constant__ AttnK a) {
+  using Tile = AtTile<kD, kF8>;
+  constexpr int kRows = 8 * kNT, kSt = Tile::kStages;
+  constexpr int kKs = kD / 16;  // 16-wide steps of the head
+  extern __shared__ unsigned char smraw[];
+  unsigned char *sm = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  float *osum = reinterpret_cast<float *>(sm + (size_t)kSt * 2 * Tile::kBytes);  // [kRows][kD]
+  float2 *wml = reinterpret_cast<float2 *>(osum + kRows * kD);                   // [warps][kRows]
+  int32_t *cum = reinterpret_cast<int32_t *>(wml + kAtWarps * kRows);            // [B + 1]
+  __shared__ __align__(8) uint64_t full[kSt], empty[kSt];
+  __shared__ int s_fail, s_scan[kAtWarps + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kAtWarps);
+    }
+    s_fail = 0;
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  long long tiles;
+  if (kPre) {
+    tiles = (long long)ceil_div(a.B * a.G, kRows) * a.H * ceil_div(a.prefix_len, kAtKeys);
+  } else {
+    int base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
+      const int b = b0 + tid;
+      int v = 0;
+      if (b < a.B) {
+        const Span s = seq_span(a, b);
+        v = s.p_tiles + s.o_tiles;
+      }
+      int inc = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (lane == 31) s_scan[warp] = inc;
+      __syncthreads();
+      int before = base;
+      for (int w = 0; w < warp; ++w) before += s_scan[w];
+      if (b < a.B) cum[b + 1] = before + inc;
+      for (int w = 0; w <= kAtWarps; ++w) base += s_scan[w];
+      __syncthreads();
+    }
+    if (tid == 0) cum[0] = 0;
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int b = tid; b <= a.B; b += kAtThreads) a.cum[b] = cum[b];
+    tiles = (long long)a.H * base;
+  }
+  __syncthreads();
+  const int ctas = kPre ? a.ctas_pre : list_ctas(tiles, gridDim.x);
+  const int c = blockIdx.x;
+  const long long t0 = c < ctas ? list_start(tiles, ctas, c) : 0;
+  const long long t1 = c < ctas ? list_start(tiles, ctas, c + 1) : 0;
+  AtWalk<kPre> w(a, cum);
+  w.seek(t0, t1);
+
+  if (warp == kAtWarps) {
+    // ---- producer: lane i loads box i of the tile's pieces
+    const int per = kAtKeys / a.box_rows;       // boxes along the keys
+    const int boxes = per * Tile::kHalves;      // of K; V as many
+    int issued = 0;
+    bool ok = true;
+    for (uint32_t it = 0; !w.done(); ++it) {
+      const int st = it % kSt;
+      const AtTileDesc d = w.tile();
+      if (it >= kSt)
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(&empty[st], ((it / kSt) - 1) & 1));
+      if (!ok) break;
+      // boxes that hold a visible key
+      const int k_lo = max(d.lo, d.key0), k_hi = min(d.hi, d.key0 + kAtKeys);
+      const int b_lo = (k_lo - d.key0) / a.box_rows;
+      const int b_hi = ceil_div(k_hi - d.key0, a.box_rows);
+      if (lane == 0)
+        mbar_expect_tx(&full[st],
+                       (uint32_t)((b_hi - b_lo) * a.box_rows * Tile::kRow * 2));
+      __syncwarp();
+      unsigned char *kt = sm + (size_t)st * 2 * Tile::kBytes;
+      for (int i = lane; i < 2 * boxes; i += 32) {
+        const int is_v = i >= boxes, j = is_v ? i - boxes : i;
+        const int half = j / per, x = j % per;
+        if (x < b_lo || x >= b_hi) continue;
+        const int key = d.key0 + x * a.box_rows;
+        const int pg = key / a.page_size, row = key - pg * a.page_size;
+        int page = d.prefix ? a.prefix_pages[pg] : a.table[(size_t)d.b * a.max_pages + pg];
+        if ((unsigned)page >= (unsigned)a.num_pages) {
+          set_status(a.status, kStatusDevice);
+          page = a.num_pages;  // outside the tensor: the copy fills zeros
+        }
+        tma_load_4d(kt + (is_v ? Tile::kBytes : 0) + half * Tile::kHalfBytes +
+                        x * a.box_rows * Tile::kHalfRow,
+                    is_v ? &tmV : &tmK, half * (Tile::kHalfRow / (kF8 ? 1 : 2)), row, d.h, page,
+                    &full[st]);
+      }
+      issued = it + 1;
+      w.next();
+    }
+    if (!ok) s_fail = 1;
+    // copies in flight land before the CTA leaves (the consumers waited for
+    // theirs unless they gave up)
+    for (int it = max(0, issued - kSt); it < issued; ++it)
+      if (!mbar_wait_sleep(&full[it % kSt], (it / kSt) & 1)) s_fail = 1;
+  } else {
+    // ---- consumers: 16 keys of each tile, kRows rows
+    const int g = lane >> 2, t4 = lane & 3;
+    const int k0 = 16 * warp;
+    // ldmatrix lane addresses: rows of matrices (0-7, 8-15 | chunk, chunk + 1)
+    const int rk = k0 + (lane & 7) + ((lane >> 3) & 1) * 8, ck = lane >> 4;
+    // the same with rows and chunks swapped (bf16 V)
+    const int rv = k0 + (lane & 7) + (lane >> 4) * 8, cv = (lane >> 3) & 1;
+    bool ok = true;
+    uint32_t qf[kNT][kKs][2];
+    float rs[kNT][2];     // score factors of rows 2 t4, 2 t4 + 1
+    float m[kNT][2], l[kNT][2];
+    float o[kKs][kNT][4];
+    bool begin = true;
+    for (uint32_t it = 0; !w.done(); ++it) {
+      const int st = it % kSt;
+      const AtTileDesc d = w.tile();
+      const int unit = w.unit;
+      if (begin) {
+        const float ks = kF8 && a.k_scale ? a.k_scale[d.h] : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          // query row of this lane's column g
+          const int r = 8 * nt + g;
+          const int R = kPre ? d.b * kRows + r : d.b * a.G + r;
+          const bool valid = kPre ? R < a.B * a.G : r < a.G;
+          const int sb = R / a.G, sg = R - sb * a.G;
+          const uint16_t *qr = a.q + (int64_t)sb * a.q_stride + (int64_t)(d.h * a.G + sg) * kD;
+          float fac = a.scale2 * ks;
+          if (kF8) {
+            // fp16 operands: the row times a power of two that puts its
+            // largest element in [2^14, 2^15) (exact for elements down to
+            // 2^-28 of it), divided out of the scores
+            uint2 v[kKs];
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < kKs; ++k) {
+              v[k] = valid ? *reinterpret_cast<const uint2 *>(qr + 16 * k + 4 * t4)
+                           : make_uint2(0, 0);
+              top = max(max(top, v[k].x & 0x7fffu), max((v[k].x >> 16) & 0x7fffu, v[k].y & 0x7fffu));
+              top = max(top, (v[k].y >> 16) & 0x7fffu);
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // exponent field e of the largest: times 2^(141 - e); two factors
+            // keep each a normal number
+            const int e = min(max((int)(top >> 7), 1), 254);
+            const int sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
+            const float f1 = __uint_as_float((uint32_t)(127 + s1) << 23);
+            const float f2 = __uint_as_float((uint32_t)(127 + s2) << 23);
+            fac *= __uint_as_float((uint32_t)(127 - s1) << 23);
+            fac *= __uint_as_float((uint32_t)(127 - s2) << 23);
+#pragma unroll
+            for (int k = 0; k < kKs; ++k) {
+              qf[nt][k][0] = pack_f16(__uint_as_float(v[k].x << 16) * f1 * f2,
+                                      __uint_as_float(v[k].x & 0xffff0000u) * f1 * f2);
+              qf[nt][k][1] = pack_f16(__uint_as_float(v[k].y << 16) * f1 * f2,
+                                      __uint_as_float(v[k].y & 0xffff0000u) * f1 * f2);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kKs; ++k) {
+              qf[nt][k][0] = valid ? *reinterpret_cast<const uint32_t *>(qr + 16 * k + 2 * t4) : 0u;
+              qf[nt][k][1] =
+                  valid ? *reinterpret_cast<const uint32_t *>(qr + 16 * k + 2 * t4 + 8) : 0u;
+            }
+          }
+          // fac belongs to row g; this lane's scores are of rows 2 t4, 2 t4 + 1
+          rs[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * t4);
+          rs[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * t4 + 4);
+          m[nt][0] = m[nt][1] = -__int_as_float(0x7f800000);
+          l[nt][0] = l[nt][1] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kKs; ++k)
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+            o[k][nt][0] = o[k][nt][1] = o[k][nt][2] = o[k][nt][3] = 0.f;
+        begin = false;
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (it / kSt) & 1));
+      const int lo = d.lo - d.key0 - k0, hi = d.hi - d.key0 - k0;  // visible of this warp's 16
+      if (ok && lo < 16 && hi > 0) {
+        unsigned char *kt = sm + (size_t)st * 2 * Tile::kBytes;
+        unsigned char *vt = kt + Tile::kBytes;
+        const uint32_t ka = smem_addr(kt), va = smem_addr(vt);
+        const bool edge = lo > 0 || hi < 16;
+        if (edge) {
+          // masked rows of V: 0 x NaN must not reach the sums
+          constexpr int kChunks = Tile::kRow / 16;
+          for (int i = lane; i < 16 * kChunks; i += 32) {
+            const int r = i / kChunks;
+            if (r < lo || r >= hi)
+              *reinterpret_cast<uint4 *>(vt + Tile::at(k0 + r, i % kChunks)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+        }
+        // scores: keys (rows g, g + 8) x query rows (columns 2 t4, 2 t4 + 1)
+        float sc[kNT][4];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+        if (!kF8) {
+#pragma unroll
+          for (int k = 0; k < kKs; ++k) {
+            uint32_t f[4];
+            ldsm4(f, ka + Tile::at(rk, 2 * k + ck));
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+              mma_bf16_16816(sc[nt], f[0], f[1], f[2], f[3], qf[nt][k][0], qf[nt][k][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kKs; k += 2) {
+            uint32_t f[4];
+            ldsm4(f, ka + Tile::at(rk, k + ck));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t x = f[2 * j], y = f[2 * j + 1];
+              const uint32_t a0 = e4m3x2_to_f16x2(x), a2 = e4m3x2_to_f16x2(x >> 16);
+              const uint32_t a1 = e4m3x2_to_f16x2(y), a3 = e4m3x2_to_f16x2(y >> 16);
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt)
+                mma_f16_16816(sc[nt], a0, a1, a2, a3, qf[nt][k + j][0], qf[nt][k + j][1]);
+            }
+          }
+        }
+        const bool in0 = !edge || (g >= lo && g < hi), in1 = !edge || (g + 8 >= lo && g + 8 < hi);
+        uint32_t p_hi[kNT][2], p_lo[kNT][2];
+        const float kNegInf = -__int_as_float(0x7f800000);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          float s[4];
+          s[0] = in0 ? sc[nt][0] * rs[nt][0] : kNegInf;
+          s[1] = in0 ? sc[nt][1] * rs[nt][1] : kNegInf;
+          s[2] = in1 ? sc[nt][2] * rs[nt][0] : kNegInf;
+          s[3] = in1 ? sc[nt][3] * rs[nt][1] : kNegInf;
+          float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], x));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], x));
+          }
+          float base[2], f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mn = fmaxf(m[nt][i], mx[i]);
+            base[i] = mn == kNegInf ? 0.f : mn;
+            f[i] = at_ex2(m[nt][i] - base[i]);
+            m[nt][i] = mn;
+          }
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = at_ex2(s[i] - base[i & 1]);
+          l[nt][0] = l[nt][0] * f[0] + (p[0] + p[2]);
+          l[nt][1] = l[nt][1] * f[1] + (p[1] + p[3]);
+          if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+            for (int k = 0; k < kKs; ++k) {
+              o[k][nt][0] *= f[0], o[k][nt][1] *= f[1];
+              o[k][nt][2] *= f[0], o[k][nt][3] *= f[1];
+            }
+          }
+          // keys x rows -> the second product's B fragment (rows' columns)
+          if (kF8) {
+            p_hi[nt][0] = transpose8(pack_f16(p[0], p[1]));
+            p_hi[nt][1] = transpose8(pack_f16(p[2], p[3]));
+          } else {
+            // bf16 in two terms: the weights keep 16 bits (one term's 2^-9
+            // would show beside the output's own rounding; the matrix work
+            // is far from bounding here)
+            const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
+            p_hi[nt][0] = transpose8(h0), p_hi[nt][1] = transpose8(h1);
+            p_lo[nt][0] = transpose8(pack_bf16(p[0] - __uint_as_float(h0 << 16),
+                                               p[1] - __uint_as_float(h0 & 0xffff0000u)));
+            p_lo[nt][1] = transpose8(pack_bf16(p[2] - __uint_as_float(h1 << 16),
+                                               p[3] - __uint_as_float(h1 & 0xffff0000u)));
+          }
+        }
+        // o (elements of the head x rows) += V^T p
+        if (!kF8) {
+#pragma unroll
+          for (int k = 0; k < kKs; ++k) {
+            uint32_t f[4];
+            ldsm4t(f, va + Tile::at(rv, 2 * k + cv));
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              mma_bf16_16816(o[k][nt], f[0], f[1], f[2], f[3], p_lo[nt][0], p_lo[nt][1]);
+              mma_bf16_16816(o[k][nt], f[0], f[1], f[2], f[3], p_hi[nt][0], p_hi[nt][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kKs; k += 2) {
+            uint32_t f[4];
+            ldsm4t(f, va + Tile::at(rk, k + ck));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // bytes: key 2t (elements 2g, 2g + 1), key 2t + 1 (the same)
+              const uint32_t x = f[2 * j], y = f[2 * j + 1];
+              const uint32_t a0 = e4m3x2_to_f16x2(__byte_perm(x, 0, 0x4420));
+              const uint32_t a1 = e4m3x2_to_f16x2(__byte_perm(x, 0, 0x4431));
+              const uint32_t a2 = e4m3x2_to_f16x2(__byte_perm(y, 0, 0x4420));
+              const uint32_t a3 = e4m3x2_to_f16x2(__byte_perm(y, 0, 0x4431));
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt)
+                mma_f16_16816(o[k + j][nt], a0, a1, a2, a3, p_hi[nt][0], p_hi[nt][1]);
+            }
+          }
+        }
+        if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (w.next()) {
+        // the unit's part is complete: join the warps and write it
+        float fac[kNT][2];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
+            if (g == 0) wml[warp * kRows + 8 * nt + 2 * t4 + i] = make_float2(m[nt][i], l[nt][i]);
+          }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 8 * nt + 2 * t4 + i;
+            float top = wml[r].x;
+            for (int x = 1; x < kAtWarps; ++x) top = fmaxf(top, wml[x * kRows + r].x);
+            fac[nt][i] = at_ex2(m[nt][i] - (top == -__int_as_float(0x7f800000) ? 0.f : top));
+          }
+        const size_t slot = (size_t)unit + c;
+        for (int x = 0; x < kAtWarps; ++x) {
+          if (warp == x) {
+#pragma unroll
+            for (int k = 0; k < kKs; ++k)
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int r = 8 * nt + 2 * t4 + (i & 1);
+                  const int e = kF8 ? 16 * k + 2 * g + (i >> 1) : 16 * k + g + 8 * (i >> 1);
+                  const float v = o[k][nt][i] * fac[nt][i & 1];
+                  float *dst = &osum[r * kD + e];
+                  *dst = x == 0 ? v : *dst + v;
+                }
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        float *op = (kPre ? a.o_pre : a.o_own) + slot * kRows * kD;
+        for (int i = tid; i < kRows * kD / 4; i += 32 * kAtWarps)
+          reinterpret_cast<float4 *>(op)[i] = reinterpret_cast<const float4 *>(osum)[i];
+        if (tid < kRows) {
+          float top = wml[tid].x, sum = 0.f;
+          for (int x = 1; x < kAtWarps; ++x) top = fmaxf(top, wml[x * kRows + tid].x);
+          const float base = top == -__int_as_float(0x7f800000) ? 0.f : top;
+          for (int x = 0; x < kAtWarps; ++x)
+            sum += wml[x * kRows + tid].y * at_ex2(wml[x * kRows + tid].x - base);
+          (kPre ? a.ml_pre : a.ml_own)[slot * kRows + tid] = make_float2(top, sum);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        begin = true;
+      }
+    }
+    if (!ok) s_fail = 1;
+  }
+  __syncthreads();
+  if (tid == 0 && s_fail) set_status(a.status, kStatusTimeout);
+}
+
+// ------------------------------------------------------------------ joining the parts
+// One warp a query row: the parts' maxima and the sink give the base, then the
+// parts' sums and outputs are added in list order (prefix first).
+template <int kD>
+__global__ void __launch_bounds__(256)
+    k_attn_combine(const __grid_constant__ AttnK a, int own_rows, int grid_own) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int q_heads = a.G * a.H;
+  if (row >= a.B * q_heads) return;
+  const int b = row / q_heads, head = row % q_heads, h = head / a.G, g = head % a.G;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  const bool has = a.lens[b] >= 0;
+  // parts of this row: prefix slots [p0, p1), own slots [s0, s1)
+  int p0 = 0, p1 = 0, s0 = 0, s1 = 0, pr = 0;
+  if (has && a.window == 0 && a.prefix_len > 0) {
+    const int R = b * a.G + g, blk = R / a.pre_rows;
+    pr = R % a.pre_rows;
+    const int n = ceil_div(a.prefix_len, kAtKeys), u = blk * a.H + h;
+    const long long tiles = (long long)ceil_div(a.B * a.G, a.pre_rows) * a.H * n;
+    const long long t = (long long)u * n;
+    p0 = u + list_cta(tiles, a.ctas_pre, t);
+    p1 = u + list_cta(tiles, a.ctas_pre, t + n - 1) + 1;
+  }
+  const int c0 = a.cum[b], n = a.cum[b + 1] - c0;
+  if (n > 0) {
+    const long long tiles = (long long)a.H * a.cum[a.B];
+    const int ctas = list_ctas(tiles, grid_own), u = b * a.H + h;
+    const long long t = (long long)a.H * c0 + (long long)h * n;
+    s0 = u + list_cta(tiles, ctas, t);
+    s1 = u + list_cta(tiles, ctas, t + n - 1) + 1;
+  }
+  const float sink = a.sinks ? a.sinks[head] * kLog2e : kNegInf;
+  float top = sink;
+  for (int i = p0 + lane; i < p1; i += 32)
+    top = fmaxf(top, ld_cg_f32(&a.ml_pre[(size_t)i * a.pre_rows + pr].x));
+  for (int i = s0 + lane; i < s1; i += 32)
+    top = fmaxf(top, ld_cg_f32(&a.ml_own[(size_t)i * own_rows + g].x));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float base = top == kNegInf ? 0.f : top;
+  constexpr int kV = kD / 32;
+  float acc[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+  float sum = at_ex2(sink - base);
+  auto add = [&](const float2 *mlp, const float *op) {
+    const float m = ld_cg_f32(&mlp->x), l = ld_cg_f32(&mlp->y);
+    const float f = at_ex2(m - base);
+    sum += f * l;
+    if (kV == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(op) + lane);
+      acc[0] += f * v.x, acc[1] += f * v.y, acc[2 % kV] += f * v.z, acc[3 % kV] += f * v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2 *>(op) + lane);
+      acc[0] += f * v.x, acc[1] += f * v.y;
+    }
+  };
+#pragma unroll 4
+  for (int i = p0; i < p1; ++i)
+    add(a.ml_pre + (size_t)i * a.pre_rows + pr, a.o_pre + ((size_t)i * a.pre_rows + pr) * kD);
+#pragma unroll 4
+  for (int i = s0; i < s1; ++i)
+    add(a.ml_own + (size_t)i * own_rows + g, a.o_own + ((size_t)i * own_rows + g) * kD);
+  const float vs = a.v_scale ? a.v_scale[h] : 1.f;
+  const float inv = sum == 0.f ? 0.f : vs / sum;
+  uint16_t *dst = a.out + (int64_t)b * a.out_stride + (int64_t)head * kD;
+  if (kV == 4)
+    reinterpret_cast<uint2 *>(dst)[lane] =
+        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
+                   pack_bf16(acc[2 % kV] * inv, acc[3 % kV] * inv));
+  else
+    reinterpret_cast<uint32_t *>(dst)[lane] = pack_bf16(acc[0] * inv, acc[1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[(size_t)b * q_heads + head] = sum == 0.f ? kNegInf : (base + log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------------ host
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode4 = nullptr;
+std::mutex g_encode4_mu;
+
+cudaError_t get_encode4() {
+  std::lock_guard<std::mutex> lock(g_encode4_mu);
+  if (g_encode4) return cudaSuccess;
+  void *fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
+  if (e != cudaSuccess) return e;
+  if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+  g_encode4 = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  return cudaSuccess;
+}
+
+// The pages as a 4-D tensor (element, row, KV head, page); boxes of one row
+// piece (at most 128 bytes) by `rows` rows.
+cudaError_t pages_map(CUtensorMap *m, const flint_kv_cache &c, const void *base, int rows) {
+  const bool f8 = c.type == FLINT_KV_E4M3;
+  const int64_t elt = f8 ? 1 : 2;
+  const int row_bytes = c.head_dim * (int)elt, box_bytes = row_bytes > 128 ? 128 : row_bytes;
+  // a dimension of one has a stride that nothing uses, but the map wants a valid one
+  const int64_t pack = (int64_t)c.head_dim * elt;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {
+      (cuuint64_t)(c.token_stride * elt),
+      (cuuint64_t)(c.heads > 1 ? c.head_stride * elt : pack),
+      (cuuint64_t)(c.num_pages > 1 ? c.page_stride * elt : pack)};
+  const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / elt), (cuuint32_t)rows, 1, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode4(
+      m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+      const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t at_launch(void (*kernel)(KArgs...), int grid, int block, size_t smem, cudaStream_t st,
+                      Args... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+template <int kD, bool kF8, int kNT, bool kPre>
+cudaError_t launch_parts(const CUtensorMap &k, const CUtensorMap &v, const AttnK &a, int grid,
+                         cudaStream_t st) {
+  using Tile = AtTile<kD, kF8>;
+  const size_t smem = 1024 + (size_t)Tile::kStages * 2 * Tile::kBytes +
+                      sizeof(float) * 8 * kNT * kD + sizeof(float2) * kAtWarps * 8 * kNT +
+                      (kPre ? 0 : sizeof(int32_t) * ((size_t)a.B + 1));
+  return at_launch(k_attn_parts<kD, kF8, kNT, kPre>, grid, kAtThreads, smem, st, k, v, a);
+}
+
+int pre_rows_of(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kAtPrefixRows; }
+
+struct AttnLayout {
+  size_t ctrl, cum, ml_own, ml_pre, o_own, o_pre, total;
+};
+AttnLayout attn_layout(int B, int q_heads, int kv_heads, int d) {
+  const int G = q_heads / kv_heads;
+  const size_t own_rows = G <= 8 ? 8 : 16;
+  const size_t pre_rows = pre_rows_of(B * G);
+  const size_t own = (size_t)B * kv_heads + kAtMaxCtas;
+  const size_t pre = (size_t)ceil_div(B * G, (int)pre_rows) * kv_heads + kAtMaxCtas;
+  AttnLayout L{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at = align256(at + bytes);
+    return r;
+  };
+  L.ctrl = take(256);
+  L.cum = take(sizeof(int32_t) * ((size_t)B + 1));
+  L.ml_own = take(sizeof(float2) * own * own_rows);
+  L.ml_pre = take(sizeof(float2) * pre * pre_rows);
+  L.o_own = take(sizeof(float) * own * own_rows * d);
+  L.o_pre = take(sizeof(float) * pre * pre_rows * d);
+  L.total = at;
+  return L;
+}
+
+template <int kD, bool kF8>
+cudaError_t launch_attn_as(const CUtensorMap &k, const CUtensorMap &v, AttnK &a, int sms,
+                           cudaStream_t st) {
+  cudaError_t e;
+  const int rows = a.B * a.G;
+  const int wide = 2 * sms < kAtMaxCtas ? 2 * sms : kAtMaxCtas;
+  if (a.prefix_len > 0 && a.window == 0) {
+    const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H *
+                            ceil_div(a.prefix_len, kAtKeys);
+    const int grid = a.pre_rows <= 16 ? wide : (sms < kAtMaxCtas ? sms : kAtMaxCtas);
+    a.ctas_pre = (int)(tiles < grid ? tiles : grid);
+    note_step("attention prefix launch");
+    e = a.pre_rows == 8    ? launch_parts<kD, kF8, 1, true>(k, v, a, a.ctas_pre, st)
+        : a.pre_rows == 16 ? launch_parts<kD, kF8, 2, true>(k, v, a, a.ctas_pre, st)
+                           : launch_parts<kD, kF8, 4, true>(k, v, a, a.ctas_pre, st);
+    if (e != cudaSuccess) return e;
+  }
+  note_step("attention launch");
+  e = a.G <= 8 ? launch_parts<kD, kF8, 1, false>(k, v, a, wide, st)
+               : launch_parts<kD, kF8, 2, false>(k, v, a, wide, st);
+  if (e != cudaSuccess) return e;
+  note_step("attention combine launch");
+  return at_launch(k_attn_combine<kD>, ceil_div(rows * a.H, 8), 256, 0, st, a, a.G <= 8 ? 8 : 16,
+                   wide);
+}
+
+}  // namespace
+
+size_t attn_ws_bytes(int B, int q_heads, int kv_heads, int head_dim) {
+  return attn_layout(B, q_heads, kv_heads, head_dim).total;
+}
+
+cudaError_t launch_attn(const AttnArgs &p, char *ws, cudaStream_t st) {
+  cudaError_t e = noted(get_encode4(), "cuTensorMapEncodeTiled entry point");
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  note_step("attention device query");
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  const AttnLayout L = attn_layout(p.B, p.q_heads, p.c.heads, p.c.head_dim);
+  AttnK a{};
+  a.q = p.q, a.q_stride = p.q_stride, a.B = p.B, a.H = p.c.heads, a.G = p.q_heads / p.c.heads;
+  a.table = p.page_table, a.max_pages = p.max_pages, a.lens = p.lens;
+  a.prefix_pages = p.prefix_pages, a.prefix_len = p.prefix_len, a.window = p.window;
+  a.page_size = p.c.page_size, a.num_pages = p.c.num_pages;
+  a.box_rows = kAtKeys;
+  while (a.page_size % a.box_rows) a.box_rows /= 2;  // >= 16: page_size is a multiple of 16
+  a.scale2 = p.scale * kLog2e;
+  const bool f8 = p.c.type == FLINT_KV_E4M3;
+  a.k_scale = f8 ? p.c.k_scale : nullptr, a.v_scale = f8 ? p.c.v_scale : nullptr;
+  a.sinks = p.sinks, a.out = p.out, a.out_stride = p.out_stride, a.lse = p.lse;
+  a.status = reinterpret_cast<uint32_t *>(ws + L.ctrl) + 1;
+  a.cum = reinterpret_cast<int32_t *>(ws + L.cum);
+  a.ml_own = reinterpret_cast<float2 *>(ws + L.ml_own);
+  a.ml_pre = reinterpret_cast<float2 *>(ws + L.ml_pre);
+  a.o_own = reinterpret_cast<float *>(ws + L.o_own);
+  a.o_pre = reinterpret_cast<float *>(ws + L.o_pre);
+  a.pre_rows = pre_rows_of(a.B * a.G);
+  CUtensorMap k, v;
+  note_step("attention tensor maps");
+  if ((e = pages_map(&k, p.c, p.c.k, a.box_rows)) != cudaSuccess ||
+      (e = pages_map(&v, p.c, p.c.v, a.box_rows)) != cudaSuccess)
+    return e;
+  if (p.c.head_dim == 128)
+    return f8 ? launch_attn_as<128, true>(k, v, a, sms, st)
+              : launch_attn_as<128, false>(k, v, a, sms, st);
+  return f8 ? launch_attn_as<64, true>(k, v, a, sms, st)
+            : launch_attn_as<64, false>(k, v, a, sms, st);
+}
+
+}  // namespace flint

@@ -184,4 +184,55 @@ cudaError_t launch_prefill(const LayerArgs &L, const uint16_t *x, int T, uint16_
 cudaError_t launch_route_many(const LayerArgs &L, const uint16_t *x, int T, int32_t *idx, float *w,
                               char *ws, cudaStream_t st);
 
+// flint_kv_append's arguments behind the checks (flint.h), the cache's among them
+struct AppendArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  int T, q_heads;
+  const int64_t *slots;
+  const int32_t *pos;
+  int rope_dim, interleaved;
+  const uint16_t *q_norm, *k_norm;
+  uint16_t *q_out;
+  int64_t q_out_stride;
+  void *kc, *vc;
+  int type, num_pages, page_size, heads, head_dim;
+  int64_t page_stride, head_stride, token_stride;
+  const float *k_scale, *v_scale;
+  uint32_t *status;
+};
+cudaError_t launch_append(const AppendArgs &a, double theta, cudaStream_t st);
+
+struct SampleArgs {
+  const float *logits;
+  int64_t stride;
+  int B, V;
+  const float *temperature;
+  const int32_t *top_k;
+  const float *top_p, *min_p, *u;
+  int32_t *token;
+  float *logprob;
+};
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st);
+
+// flint_attn_decode's arguments behind the checks (flint.h)
+struct AttnArgs {
+  flint_kv_cache c;
+  const uint16_t *q;
+  int64_t q_stride;
+  int B, q_heads;
+  const int32_t *page_table;
+  int max_pages;
+  const int32_t *lens, *prefix_pages;
+  int prefix_len;
+  float scale;
+  int window;
+  const float *sinks;
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;
+};
+size_t attn_ws_bytes(int B, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_attn(const AttnArgs &a, char *ws, cudaStream_t st);
+
 }  // namespace flint
