@@ -15,54 +15,18 @@
 // sequences' lengths.  A unit that falls to several CTAs is summed from their
 // parts by k_attn_combine; part (unit u, CTA c) is written to slot u + c,
 // which no two parts share since the list advances in u or c at each part.
-#include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <mutex>
 
-#include "common.cuh"
-#include "internal.h"
+#include "attn.cuh"
 
 namespace flint {
 
 constexpr int kAtKeys = 64;       // keys of a tile
 constexpr int kAtWarps = 4;       // consumer warps, 16 keys of each tile each
 constexpr int kAtThreads = 32 * (kAtWarps + 1);
-constexpr int kAtMaxCtas = 512;
-constexpr int kAtPrefixRows = 32;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-FLINT_DEV float at_ex2(float x) {
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// ------------------------------------------------------------------ the plan
-struct AttnK {
-  const uint16_t *q;
-  int64_t q_stride;
-  int B, G, H;               // sequences, query heads a KV head, KV heads
-  const int32_t *table;
-  int max_pages;
-  const int32_t *lens, *prefix_pages;
-  int prefix_len, window;
-  int page_size, num_pages, box_rows;
-  float scale2;              // scale * log2(e)
-  const float *k_scale, *v_scale, *sinks;
-  uint16_t *out;
-  int64_t out_stride;
-  float *lse;
-  uint32_t *status;
-  int32_t *cum;              // [B + 1] running tiles of the sequences (one KV head)
-  float *o_own, *o_pre;      // parts: [slot][rows][D], and their (max, sum)
-  float2 *ml_own, *ml_pre;
-  int ctas_pre;              // CTAs of the prefix list
-  int pre_rows;              // rows of a prefix unit
-};
+constexpr int kAtSmallRows = 16;  // rows of a batch whose prefix needs no tcgen05 tile
 
 // The part of the keys that sequence b's row sees, as 64-key tiles.
 struct Span {
@@ -97,18 +61,6 @@ FLINT_DEV Span seq_span(const AttnK &a, int b) {
   s.o_tiles = n > 0 ? ceil_div(n, kAtKeys) - s.o_lo / kAtKeys : 0;
   return s;
 }
-FLINT_DEV int list_ctas(long long tiles, int grid) {
-  return (int)(tiles < grid ? (tiles > 0 ? tiles : 1) : grid);
-}
-FLINT_DEV long long list_start(long long tiles, int ctas, int c) { return tiles * c / ctas; }
-// the CTA that holds tile t
-FLINT_DEV int list_cta(long long tiles, int ctas, long long t) {
-  int c = (int)(t * ctas / tiles);
-  while (c + 1 < ctas && list_start(tiles, ctas, c + 1) <= t) ++c;
-  while (c > 0 && list_start(tiles, ctas, c) > t) --c;
-  return c;
-}
-
 // ------------------------------------------------------------------ matrix pieces
 FLINT_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -140,24 +92,10 @@ FLINT_DEV uint32_t e4m3x2_to_f16x2(uint32_t v) {
   asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(v));
   return d;
 }
-FLINT_DEV uint32_t pack_bf16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 FLINT_DEV uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
-}
-
-FLINT_DEV void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
-                           uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-      : "memory");
 }
 
 // ------------------------------------------------------------------ parts kernel
@@ -256,7 +194,7 @@ struct AtWalk {
 
 // kRows = 8 kNT query rows a unit
 template <int kD, bool kF8, int kNT, bool kPre>
-__global__ void __launch_bounds__(kAtThreads, kNT <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kAtThreads, 2)
     k_attn_parts(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ AttnK a) {
   using Tile = AtTile<kD, kF8>;
@@ -278,7 +216,9 @@ __global__ void __launch_bounds__(kAtThreads, kNT <= 2 ? 2 : 1)
     }
     s_fail = 0;
   }
-  pdl_wait();
+  // Behind a prefix kernel, which waited for all that came before it, only the
+  // end waits: this kernel's CTAs fill the SMs that the prefix's leave.
+  if (kPre || !a.behind_prefix) pdl_wait();
   pdl_trigger();
 
   long long tiles;
@@ -638,6 +578,7 @@ __global__ void __launch_bounds__(kAtThreads, kNT <= 2 ? 2 : 1)
   }
   __syncthreads();
   if (tid == 0 && s_fail) set_status(a.status, kStatusTimeout);
+  if (!kPre && a.behind_prefix) pdl_wait();
 }
 
 // ------------------------------------------------------------------ joining the parts
@@ -660,7 +601,7 @@ __global__ void __launch_bounds__(256)
   if (has && a.window == 0 && a.prefix_len > 0) {
     const int R = b * a.G + g, blk = R / a.pre_rows;
     pr = R % a.pre_rows;
-    const int n = ceil_div(a.prefix_len, kAtKeys), u = blk * a.H + h;
+    const int n = ceil_div(a.prefix_len, a.pre_keys), u = blk * a.H + h;
     const long long tiles = (long long)ceil_div(a.B * a.G, a.pre_rows) * a.H * n;
     const long long t = (long long)u * n;
     p0 = u + list_cta(tiles, a.ctas_pre, t);
@@ -737,8 +678,8 @@ cudaError_t get_encode4() {
   return cudaSuccess;
 }
 
-// The pages as a 4-D tensor (element, row, KV head, page); boxes of one row
-// piece (at most 128 bytes) by `rows` rows.
+}  // namespace
+
 cudaError_t pages_map(CUtensorMap *m, const flint_kv_cache &c, const void *base, int rows) {
   const bool f8 = c.type == FLINT_KV_E4M3;
   const int64_t elt = f8 ? 1 : 2;
@@ -760,6 +701,8 @@ cudaError_t pages_map(CUtensorMap *m, const flint_kv_cache &c, const void *base,
       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+namespace {
 
 template <typename... KArgs, typename... Args>
 cudaError_t at_launch(void (*kernel)(KArgs...), int grid, int block, size_t smem, cudaStream_t st,
@@ -792,7 +735,9 @@ cudaError_t launch_parts(const CUtensorMap &k, const CUtensorMap &v, const AttnK
   return at_launch(k_attn_parts<kD, kF8, kNT, kPre>, grid, kAtThreads, smem, st, k, v, a);
 }
 
-int pre_rows_of(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : kAtPrefixRows; }
+int pre_rows_of(int rows) {
+  return rows <= 8 ? 8 : rows <= kAtSmallRows ? kAtSmallRows : rows <= 128 ? 128 : 256;
+}
 
 struct AttnLayout {
   size_t ctrl, cum, ml_own, ml_pre, o_own, o_pre, total;
@@ -802,7 +747,8 @@ AttnLayout attn_layout(int B, int q_heads, int kv_heads, int d) {
   const size_t own_rows = G <= 8 ? 8 : 16;
   const size_t pre_rows = pre_rows_of(B * G);
   const size_t own = (size_t)B * kv_heads + kAtMaxCtas;
-  const size_t pre = (size_t)ceil_div(B * G, (int)pre_rows) * kv_heads + kAtMaxCtas;
+  const size_t pre = (size_t)ceil_div(B * G, (int)pre_rows) * kv_heads +
+                     (pre_rows <= kAtSmallRows ? kAtMaxCtas : kAtPreCtas);
   AttnLayout L{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -821,20 +767,24 @@ AttnLayout attn_layout(int B, int q_heads, int kv_heads, int d) {
 }
 
 template <int kD, bool kF8>
-cudaError_t launch_attn_as(const CUtensorMap &k, const CUtensorMap &v, AttnK &a, int sms,
-                           cudaStream_t st) {
+cudaError_t launch_attn_as(const flint_kv_cache &c, const CUtensorMap &k, const CUtensorMap &v,
+                           AttnK &a, int sms, cudaStream_t st) {
   cudaError_t e;
   const int rows = a.B * a.G;
   const int wide = 2 * sms < kAtMaxCtas ? 2 * sms : kAtMaxCtas;
-  if (a.prefix_len > 0 && a.window == 0) {
-    const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H *
-                            ceil_div(a.prefix_len, kAtKeys);
-    const int grid = a.pre_rows <= 16 ? wide : (sms < kAtMaxCtas ? sms : kAtMaxCtas);
-    a.ctas_pre = (int)(tiles < grid ? tiles : grid);
-    note_step("attention prefix launch");
-    e = a.pre_rows == 8    ? launch_parts<kD, kF8, 1, true>(k, v, a, a.ctas_pre, st)
-        : a.pre_rows == 16 ? launch_parts<kD, kF8, 2, true>(k, v, a, a.ctas_pre, st)
-                           : launch_parts<kD, kF8, 4, true>(k, v, a, a.ctas_pre, st);
+  a.behind_prefix = a.prefix_len > 0 && a.window == 0;
+  if (a.behind_prefix) {
+    if (a.pre_rows <= kAtSmallRows) {
+      const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H *
+                              ceil_div(a.prefix_len, kAtKeys);
+      a.pre_keys = kAtKeys;
+      a.ctas_pre = (int)(tiles < wide ? tiles : wide);
+      note_step("attention prefix launch");
+      e = a.pre_rows == 8 ? launch_parts<kD, kF8, 1, true>(k, v, a, a.ctas_pre, st)
+                          : launch_parts<kD, kF8, 2, true>(k, v, a, a.ctas_pre, st);
+    } else {
+      e = launch_attn_prefix(c, a, sms, st);
+    }
     if (e != cudaSuccess) return e;
   }
   note_step("attention launch");
@@ -885,10 +835,10 @@ cudaError_t launch_attn(const AttnArgs &p, char *ws, cudaStream_t st) {
       (e = pages_map(&v, p.c, p.c.v, a.box_rows)) != cudaSuccess)
     return e;
   if (p.c.head_dim == 128)
-    return f8 ? launch_attn_as<128, true>(k, v, a, sms, st)
-              : launch_attn_as<128, false>(k, v, a, sms, st);
-  return f8 ? launch_attn_as<64, true>(k, v, a, sms, st)
-            : launch_attn_as<64, false>(k, v, a, sms, st);
+    return f8 ? launch_attn_as<128, true>(p.c, k, v, a, sms, st)
+              : launch_attn_as<128, false>(p.c, k, v, a, sms, st);
+  return f8 ? launch_attn_as<64, true>(p.c, k, v, a, sms, st)
+            : launch_attn_as<64, false>(p.c, k, v, a, sms, st);
 }
 
 }  // namespace flint

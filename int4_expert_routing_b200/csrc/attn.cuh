@@ -1,0 +1,81 @@
+// What the decode-attention kernels share: the call's arguments, the list of
+// tiles that the CTAs of a kernel divide, and small device pieces.
+#pragma once
+#include <cuda.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace flint {
+
+constexpr int kAtMaxCtas = 512;
+constexpr int kAtPreCtas = 160;   // of the tensor-core prefix kernel
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------ the plan
+struct AttnK {
+  const uint16_t *q;
+  int64_t q_stride;
+  int B, G, H;               // sequences, query heads a KV head, KV heads
+  const int32_t *table;
+  int max_pages;
+  const int32_t *lens, *prefix_pages;
+  int prefix_len, window;
+  int page_size, num_pages, box_rows;
+  float scale2;              // scale * log2(e)
+  const float *k_scale, *v_scale, *sinks;
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;
+  uint32_t *status;
+  int32_t *cum;              // [B + 1] running tiles of the sequences (one KV head)
+  float *o_own, *o_pre;      // parts: [slot][rows][D], and their (max, sum)
+  float2 *ml_own, *ml_pre;
+  int ctas_pre;              // CTAs of the prefix list
+  int pre_rows, pre_keys;    // rows of a prefix unit, keys of its tiles
+  int behind_prefix;         // the own keys' kernel follows a prefix kernel
+};
+
+// A list of tiles over `ctas` CTAs: CTA c takes tiles [c n / N, (c + 1) n / N).
+FLINT_DEV int list_ctas(long long tiles, int grid) {
+  return (int)(tiles < grid ? (tiles > 0 ? tiles : 1) : grid);
+}
+FLINT_DEV long long list_start(long long tiles, int ctas, int c) { return tiles * c / ctas; }
+// the CTA that holds tile t
+FLINT_DEV int list_cta(long long tiles, int ctas, long long t) {
+  int c = (int)(t * ctas / tiles);
+  while (c + 1 < ctas && list_start(tiles, ctas, c + 1) <= t) ++c;
+  while (c > 0 && list_start(tiles, ctas, c) > t) --c;
+  return c;
+}
+
+FLINT_DEV float at_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+FLINT_DEV uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+FLINT_DEV void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
+                           uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// launches the prefix kernel on the tensor cores (attn_prefix.cu)
+cudaError_t launch_attn_prefix(const flint_kv_cache &c, AttnK &a, int sms, cudaStream_t st);
+// the pages as a 4-D tensor (element, row, KV head, page), boxes of one piece
+// of a row (at most 128 bytes) by `rows` rows
+cudaError_t pages_map(CUtensorMap *m, const flint_kv_cache &c, const void *base, int rows);
+
+}  // namespace flint

@@ -1,0 +1,554 @@
+// The shared prefix of flint_attn_decode on the tensor cores: rows of many
+// sequences against keys that all of them see.
+//
+// A unit is up to 256 query rows of one KV head (two blocks A and B of 128)
+// over the prefix in tiles of 128 keys; the CTAs of a persistent kernel share
+// the units' tiles evenly (attn.cuh).  For each tile and block
+//   S = Q K^T      tcgen05, Q and K from shared memory, S to tensor memory;
+//   P = 2^(S f - m) one thread a row: no shuffles; P replaces S;
+//   O += P V       tcgen05, P from tensor memory, V as it lies in its page
+//                  (keys x elements: the "MN-major" operand), O stays in
+//                  tensor memory for the whole unit.
+// The blocks alternate: while one's exponentials run, the tensor cores have
+// the other's two products.  The issue order O_x(j-1), S_x(j), commit makes
+// one barrier say both that S_x(j) is there and that O_x may be rescaled.
+// The maximum m is moved (and O rescaled, by the row's own thread) only when
+// it grows by more than 2^8, since any base gives the same quotient and fp32
+// has the room; that is rare after the first tile.
+//
+// Weights enter the second product as bf16 (fp16 with the 8-bit cache): one
+// rounding of 2^-9 each, where a second term would add half as many products
+// again to a kernel that they bound.  Sums and statistics are fp32.
+//
+// The 8-bit cache: E4M3 codes are exact in fp16, so four warps convert each
+// tile once for both blocks; Q is scaled into fp16 by a power of two a row,
+// which f divides out.
+#include "attn.cuh"
+#include "tensor.cuh"
+
+namespace flint {
+
+namespace {
+
+constexpr int kPkKeys = 128;                 // keys of a tile
+
+template <int kD, bool kF8>
+struct PreCfg {
+  static constexpr int kThreads = kF8 ? 512 : 384;
+  static constexpr int kAtoms = kD / 64;                  // 128-byte pieces of a row
+  static constexpr int kAtom = kPkKeys * 128;             // bytes of 128 rows of one
+  static constexpr int kTile = kAtoms * kAtom;            // K or V of a tile, 16-bit
+  static constexpr int kSlots = kD == 128 ? (kF8 ? 4 : 5) : 8;
+  static constexpr int kRaw = kF8 ? (kD == 128 ? 2 : 4) : 0;
+  static constexpr int kRawTile = kPkKeys * kD;
+  static constexpr int kQ = 2 * kTile;
+  static constexpr size_t kSmem = 1024 + kQ + kSlots * kTile + kRaw * kRawTile;
+  // registers: softmax warps, the others; below the launch's total
+  static constexpr int kRegSoft = kF8 ? 184 : 208, kRegCtl = kF8 ? 72 : 88;
+  static constexpr int kRegLaunch = kF8 ? 128 : 168;
+  static_assert(256 * kRegSoft + (kThreads - 256) * kRegCtl <= kThreads * kRegLaunch, "registers");
+};
+
+// D (tensor memory, 128 lanes) += A (tensor memory, 16-bit pairs) B (shared memory)
+FLINT_DEV void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, "
+      "%3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accum));
+}
+// Shared-memory descriptor of an operand whose rows are its K dimension, in
+// 128-byte swizzle: 8-row groups 1,024 bytes apart, 64-element pieces of a
+// row `piece` bytes apart.
+FLINT_DEV uint64_t sw128_mn_desc(uint32_t saddr, uint32_t piece) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(piece >> 4) << 16) | (64ull << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// keeps uses of loaded registers behind the wait
+FLINT_DEV void pin32(uint32_t *v) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+}
+FLINT_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+FLINT_DEV uint64_t pair2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+FLINT_DEV void unpair2(uint64_t d, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
+}
+FLINT_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+FLINT_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+FLINT_DEV uint32_t pk_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+FLINT_DEV uint32_t e4m3x2_f16x2(uint32_t v) {
+  uint32_t d;
+  asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(v));
+  return d;
+}
+
+// A CTA's stretch of one unit: tiles [j0, j1) of n.
+struct PreRun {
+  int unit, blk, h, j0, j1;
+};
+FLINT_DEV bool pre_run(const AttnK &a, int n, long long &t, long long t1, PreRun &r) {
+  if (t >= t1) return false;
+  r.unit = (int)(t / n);
+  r.j0 = (int)(t - (long long)r.unit * n);
+  const long long left = t1 - t;
+  r.j1 = left < n - r.j0 ? r.j0 + (int)left : n;
+  r.blk = r.unit / a.H, r.h = r.unit % a.H;
+  t += r.j1 - r.j0;
+  return true;
+}
+
+template <int kD, bool kF8>
+__global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
+    k_attn_prefix(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ AttnK a, int box_rows, float scale2, uint32_t q_sign) {
+  using C = PreCfg<kD, kF8>;
+  extern __shared__ unsigned char smraw[];
+  unsigned char *sm = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  unsigned char *slots = sm + C::kQ, *raw = slots + C::kSlots * C::kTile;
+  __shared__ __align__(8) uint64_t full[C::kSlots], empty[C::kSlots];
+  __shared__ __align__(8) uint64_t rfull[kF8 ? C::kRaw : 1], rempty[kF8 ? C::kRaw : 1];
+  __shared__ __align__(8) uint64_t sfull[2], pready[2], ofull[2], qready[2], done;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&full[s], kF8 ? 4 : 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rempty[s], 4);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sfull[x], 1);
+      mbar_init(&pready[x], 4);
+      mbar_init(&ofull[x], 1);
+      mbar_init(&qready[x], 4);
+    }
+    mbar_init(&done, 1);
+    s_fail = 0;
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&s_tmem)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;  // columns: S_A 0, S_B 128, O_A 256, O_B 384
+  pdl_wait();
+  pdl_trigger();
+  const int rows = a.B * a.G, n = ceil_div(a.prefix_len, kPkKeys);
+  const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H * n;
+  long long t = list_start(tiles, gridDim.x, blockIdx.x);
+  const long long t1 = list_start(tiles, gridDim.x, blockIdx.x + 1);
+  PreRun r;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegCtl));
+    if (warp == 8) {
+      // ---- producer: lane i loads box i (of 16 at most) of K, then of V
+      constexpr int kRing = kF8 ? C::kRaw : C::kSlots;
+      constexpr int kBytes = kF8 ? C::kRawTile : C::kTile;
+      constexpr int kPieces = kF8 ? 1 : C::kAtoms;           // boxes along a row
+      constexpr int kRow = kF8 ? kD : 128;                   // bytes of a box's row
+      uint64_t *fl = kF8 ? rfull : full, *em = kF8 ? rempty : empty;
+      unsigned char *ring = kF8 ? raw : slots;
+      uint32_t k = 0;
+      bool ok = true;
+      while (ok && pre_run(a, n, t, t1, r)) {
+        for (int j = r.j0; j < r.j1 && ok; ++j) {
+          const int boxes = ceil_div(min(kPkKeys, a.prefix_len - j * kPkKeys), box_rows);
+          const int piece = lane / boxes, x = lane - piece * boxes;
+          int page = 0, row = 0;
+          if (piece < kPieces) {
+            const int key = j * kPkKeys + x * box_rows, pg = key / a.page_size;
+            row = key - pg * a.page_size;
+            page = a.prefix_pages[pg];
+            if ((unsigned)page >= (unsigned)a.num_pages) {
+              set_status(a.status, kStatusDevice);
+              page = a.num_pages;  // outside the tensor: the copy fills zeros
+            }
+          }
+          for (int v = 0; v < 2; ++v, ++k) {
+            const int s = k % kRing;
+            if (k >= (uint32_t)kRing)
+              ok = __all_sync(0xffffffffu, mbar_wait_sleep(&em[s], ((k / kRing) - 1) & 1));
+            if (!ok) break;
+            if (lane == 0)
+              mbar_expect_tx(&fl[s], (uint32_t)(boxes * box_rows * kRow * kPieces));
+            __syncwarp();
+            if (piece < kPieces)
+              tma_load_4d(ring + (size_t)s * kBytes + piece * C::kAtom + x * box_rows * kRow,
+                          v ? &tmV : &tmK, piece * 64, row, r.h, page, &fl[s]);
+          }
+        }
+      }
+      if (!ok) s_fail = 1;
+      // copies in flight land before the CTA leaves
+      for (uint32_t i = k > (uint32_t)kRing ? k - kRing : 0; i < k; ++i)
+        if (!mbar_wait_sleep(&fl[i % kRing], (i / kRing) & 1)) s_fail = 1;
+    } else if (warp == 9) {
+      // ---- products
+      constexpr uint32_t kType = kF8 ? 0u : 1u;  // f16, bf16
+      // f32 result, M = 128; S: N = 128, both K-major; O: N = D, B rows = keys
+      constexpr uint32_t kBase = (1u << 4) | (kType << 7) | (kType << 10) | (8u << 24);
+      constexpr uint32_t kDescS = kBase | ((uint32_t)(kPkKeys >> 3) << 17);
+      constexpr uint32_t kDescO = kBase | (1u << 16) | ((uint32_t)(kD >> 3) << 17);
+      uint32_t k = 0;              // K slot 2 i, V slot 2 i + 1 of tile i
+      uint32_t np[2] = {0, 0};     // P tiles taken of block x
+      uint32_t nq[2] = {0, 0};     // units begun by block x
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+      };
+      // O_x (+)= P V of tile i, whose key count is `keys`
+      auto product_o = [&](int x, uint32_t i, int keys, bool first) {
+        wait(&pready[x], np[x] & 1);
+        ++np[x];
+        const uint32_t sv = (2 * i + 1) % C::kSlots;
+        if (!ok) return;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t va = smem_addr(slots + sv * C::kTile);
+          const int steps = (keys + 15) / 16;
+          for (int q = 0; q < steps; ++q)
+            umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * q,
+                    sw128_mn_desc(va + 2048 * q, C::kAtom), kDescO, !first || q > 0);
+        }
+        __syncwarp();
+      };
+      // V of tile i is there; rows behind the last key of its last 16 hold
+      // what the page holds, which must not reach the sums even times 0
+      auto wait_v = [&](uint32_t i, int keys) {
+        const uint32_t m = 2 * i + 1, sv = m % C::kSlots;
+        wait(&full[sv], (m / C::kSlots) & 1);
+        if (!kF8 && ok && (keys & 15)) {
+          const int lo = keys, hi = (keys + 15) & ~15;
+          unsigned char *vt = slots + sv * C::kTile;
+          for (int c = lane; c < (hi - lo) * 8 * C::kAtoms; c += 32) {
+            const int row = lo + c / (8 * C::kAtoms), at = c % (8 * C::kAtoms);
+            *reinterpret_cast<uint4 *>(vt + (at >> 3) * C::kAtom + row * 128 + ((at & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_async();
+          __syncwarp();
+        }
+      };
+      while (ok && pre_run(a, n, t, t1, r)) {
+        const int nb = rows - r.blk * a.pre_rows > 128 ? 2 : 1;
+        for (int x = 0; x < nb; ++x) wait(&qready[x], nq[x]++ & 1);
+        int last_keys = kPkKeys;
+        for (int j = r.j0; j < r.j1 && ok; ++j, ++k) {
+          const uint32_t sk = (2 * k) % C::kSlots;
+          wait(&full[sk], ((2 * k) / C::kSlots) & 1);
+          if (j > r.j0) wait_v(k - 1, kPkKeys);
+          for (int x = 0; x < nb && ok; ++x) {
+            if (j > r.j0) product_o(x, k - 1, kPkKeys, j - 1 == r.j0);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t qa = smem_addr(sm + x * C::kTile), ka = smem_addr(slots + sk * C::kTile);
+#pragma unroll
+              for (int q = 0; q < kD / 16; ++q) {
+                const uint32_t off = (q >> 2) * C::kAtom + (q & 3) * 32;
+                umma_bf16_ss(tmem + 128 * x, sw128_desc(qa + off), sw128_desc(ka + off), kDescS,
+                             q > 0);
+              }
+              umma_commit1(&sfull[x]);
+              if (x + 1 == nb) {
+                umma_commit1(&empty[sk]);
+                if (j > r.j0) umma_commit1(&empty[(2 * k - 1) % C::kSlots]);
+              }
+            }
+            __syncwarp();
+          }
+          last_keys = min(kPkKeys, a.prefix_len - j * kPkKeys);
+        }
+        if (ok) wait_v(k - 1, last_keys);
+        for (int x = 0; x < nb && ok; ++x) {
+          product_o(x, k - 1, last_keys, r.j1 - r.j0 == 1);
+          if (ok && lane == 0) {
+            umma_commit1(&ofull[x]);
+            if (x + 1 == nb) umma_commit1(&empty[(2 * k - 1) % C::kSlots]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) s_fail = 1;
+      if (lane == 0) umma_commit1(&done);  // every product completes before tensor memory is freed
+      __syncwarp();
+      if (!mbar_wait(&done, 0)) s_fail = 1;
+    } else if (kF8 && warp >= 12) {
+      // ---- E4M3 -> fp16, a tile of K, then of V; eight lanes take one chunk
+      // of eight rows, which the two swizzles spread over all banks
+      const int ct = tid - 384;
+      uint32_t k = 0;
+      bool ok = true;
+      while (ok && pre_run(a, n, t, t1, r)) {
+        for (int j = r.j0; j < r.j1 && ok; ++j) {
+          const int keys = min(kPkKeys, a.prefix_len - j * kPkKeys);
+          for (int v = 0; v < 2 && ok; ++v, ++k) {
+            const int s = k % C::kSlots, rs = k % (kF8 ? C::kRaw : 1);
+            ok = mbar_wait_sleep(&rfull[rs], (k / (kF8 ? C::kRaw : 1)) & 1) &&
+                 (k < (uint32_t)C::kSlots || mbar_wait_sleep(&empty[s], ((k / C::kSlots) - 1) & 1));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const unsigned char *src = raw + (size_t)rs * C::kRawTile;
+            unsigned char *dst = slots + (size_t)s * C::kTile;
+            constexpr int kChunks = kD / 16;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+              const int row = ct, c = i;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (row < keys)
+                w = *reinterpret_cast<const uint4 *>(
+                    src + (kD == 128 ? row * 128 + ((c ^ (row & 7)) << 4)
+                                     : row * 64 + ((c ^ ((row >> 1) & 3)) << 4)));
+              unsigned char *d = dst + (c >> 2) * C::kAtom + row * 128;
+              const int c0 = 2 * (c & 3);
+              *reinterpret_cast<uint4 *>(d + ((c0 ^ (row & 7)) << 4)) =
+                  make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y),
+                             e4m3x2_f16x2(w.y >> 16));
+              *reinterpret_cast<uint4 *>(d + (((c0 + 1) ^ (row & 7)) << 4)) =
+                  make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w),
+                             e4m3x2_f16x2(w.w >> 16));
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&full[s]);
+              mbar_arrive(&rempty[rs]);
+            }
+          }
+        }
+      }
+      if (!ok) s_fail = 1;
+    }
+  } else {
+    // ---- softmax: thread = row 32 (warp % 4) + lane of block x
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
+    const int x = warp >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
+    const float kNegInf = -__int_as_float(0x7f800000);
+    uint32_t ns = 0, nu = 0;
+    bool ok = true;
+    while (ok && pre_run(a, n, t, t1, r)) {
+      const int R0 = r.blk * a.pre_rows + 128 * x, R = R0 + row;
+      const bool active = R0 < rows && 128 * x < a.pre_rows, valid = active && R < rows;
+      float fac = scale2;
+      if (active) {
+        // this row of Q, in the operand's swizzle
+        const int sb = R / a.G, sg = R - sb * a.G;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            a.q + (int64_t)(valid ? sb : 0) * a.q_stride + (int64_t)(r.h * a.G + (valid ? sg : 0)) * kD);
+        unsigned char *q = sm + x * C::kTile + row * 128;
+        uint4 w[kD / 8];
+#pragma unroll
+        for (int c = 0; c < kD / 8; ++c) w[c] = valid ? src[c] : make_uint4(0, 0, 0, 0);
+        float f1 = 1.f, f2 = 1.f;
+        if (kF8) {
+          fac *= a.k_scale ? a.k_scale[r.h] : 1.f;
+          // the power of two that puts the row's largest element in [2^14, 2^15)
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < kD / 8; ++c) {
+            const uint32_t y[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, max(y[i] & 0x7fffu, (y[i] >> 16) & 0x7fffu));
+          }
+          const int e = min(max((int)(top >> 7), 1), 254), sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
+          f1 = __uint_as_float((uint32_t)(127 + s1) << 23);
+          f2 = __uint_as_float((uint32_t)(127 + s2) << 23);
+          fac *= __uint_as_float((uint32_t)(127 - s1) << 23);
+          fac *= __uint_as_float((uint32_t)(127 - s2) << 23);
+        }
+#pragma unroll
+        for (int c = 0; c < kD / 8; ++c) {
+          uint32_t y[4] = {w[c].x ^ q_sign, w[c].y ^ q_sign, w[c].z ^ q_sign, w[c].w ^ q_sign};
+          if (kF8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = pk_f16(__uint_as_float(y[i] << 16) * f1 * f2,
+                            __uint_as_float(y[i] & 0xffff0000u) * f1 * f2);
+          }
+          *reinterpret_cast<uint4 *>(q + (c >> 3) * C::kAtom + (((c & 7) ^ (row & 7)) << 4)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      if (!active) continue;
+      fence_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qready[x]);
+      float m = kNegInf;
+      uint64_t l2a = 0, l2b = 0;  // fp32 pairs
+      for (int j = r.j0; j < r.j1; ++j, ++ns) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[x], ns & 1));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, v + 32 * c);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) pin32(v + 32 * c);
+        const int keys = a.prefix_len - j * kPkKeys;  // below 128 in the last tile only
+        if (keys < kPkKeys) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= keys) v[i] = 0xff800000u;
+        }
+        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int i = 0; i < 128; i += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(v[i + 2 * y])),
+                          __uint_as_float(v[i + 2 * y + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * fac;
+        const bool grow = top > m + 8.f;
+        if (j == r.j0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? at_ex2(m - top) : 1.f;
+          if (grow) m = top;
+          l2a = fma2(l2a, pair2(f, f), 0);
+          l2b = fma2(l2b, pair2(f, f), 0);
+#pragma unroll 1
+          for (int c = 0; c < kD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_async(to + 32 * c, o);
+            tmem_wait_ld();
+            pin32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(to + 32 * c, o);
+          }
+        }
+        const float base = m == kNegInf ? 0.f : m;
+        const uint64_t fac2 = pair2(fac, fac), nb2 = pair2(-base, -base);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = 64 * c + 2 * i;
+            float p0, p1;
+            unpair2(fma2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), fac2, nb2), p0, p1);
+            p0 = at_ex2(p0), p1 = at_ex2(p1);
+            if (i & 1) l2b = add2(l2b, pair2(p0, p1));
+            else l2a = add2(l2a, pair2(p0, p1));
+            p[i] = kF8 ? pk_f16(p0, p1) : pack_bf16(p0, p1);
+          }
+          tmem_st32(ts + 32 * c, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[x]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&ofull[x], nu & 1));
+      ++nu;
+      if (!ok) break;
+      tc_fence_after();
+      float l0, l1, l;
+      unpair2(add2(l2a, l2b), l0, l1);
+      l = l0 + l1;
+      const size_t at = ((size_t)r.unit + blockIdx.x) * a.pre_rows + 128 * x + row;
+      if (valid) a.ml_pre[at] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < kD / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32_async(to + 32 * c, o);
+        tmem_wait_ld();
+        pin32(o);
+        if (valid) {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.o_pre + at * kD + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+    }
+    if (!ok) s_fail = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (s_fail && tid == 0) set_status(a.status, kStatusTimeout);
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+template <int kD, bool kF8>
+cudaError_t launch_as(const CUtensorMap &k, const CUtensorMap &v, const AttnK &a, int box_rows,
+                      cudaStream_t st) {
+  using C = PreCfg<kD, kF8>;
+  cudaError_t e = cudaFuncSetAttribute(k_attn_prefix<kD, kF8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas_pre);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // a negative scale goes into the signs of Q, so that the largest score has
+  // the largest product
+  return cudaLaunchKernelEx(&cfg, k_attn_prefix<kD, kF8>, k, v, a, box_rows, fabsf(a.scale2),
+                            a.scale2 < 0.f ? 0x80008000u : 0u);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefix(const flint_kv_cache &c, AttnK &a, int sms, cudaStream_t st) {
+  int box_rows = kPkKeys;
+  while (a.page_size % box_rows) box_rows /= 2;  // >= 16: page_size is a multiple of 16
+  CUtensorMap k, v;
+  cudaError_t e;
+  note_step("attention prefix tensor maps");
+  if ((e = pages_map(&k, c, c.k, box_rows)) != cudaSuccess ||
+      (e = pages_map(&v, c, c.v, box_rows)) != cudaSuccess)
+    return e;
+  const long long tiles = (long long)ceil_div(a.B * a.G, a.pre_rows) * a.H *
+                          ceil_div(a.prefix_len, kPkKeys);
+  const int grid = sms < kAtPreCtas ? sms : kAtPreCtas;
+  a.pre_keys = kPkKeys;
+  a.ctas_pre = (int)(tiles < grid ? tiles : grid);
+  note_step("attention prefix launch");
+  if (c.head_dim == 128)
+    return c.type == FLINT_KV_E4M3 ? launch_as<128, true>(k, v, a, box_rows, st)
+                                   : launch_as<128, false>(k, v, a, box_rows, st);
+  return c.type == FLINT_KV_E4M3 ? launch_as<64, true>(k, v, a, box_rows, st)
+                                 : launch_as<64, false>(k, v, a, box_rows, st);
+}
+
+}  // namespace flint
