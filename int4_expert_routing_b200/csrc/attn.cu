@@ -12,7 +12,11 @@
 //     the whole prefix, so that a key is read once for all of them.
 // The tiles of all units form one list, which the CTAs of a persistent kernel
 // share evenly: CTA c takes tiles [c n / N, (c + 1) n / N), whatever the
-// sequences' lengths.  A unit that falls to several CTAs is summed from their
+// sequences' lengths; an own unit counts one tile more than it has, for its
+// start and end (loading Q, joining the warps, writing the part), so that a
+// CTA does not get twenty sequences of one tile where another gets one of
+// twenty (256 sequences of 1 to 1,024 keys: 112 us without, 4x the floor).
+// A unit that falls to several CTAs is summed from their
 // parts by k_attn_combine; part (unit u, CTA c) is written to slot u + c,
 // which no two parts share since the list advances in u or c at each part.
 #include <cudaTypedefs.h>
@@ -26,6 +30,7 @@ namespace flint {
 constexpr int kAtKeys = 64;       // keys of a tile
 constexpr int kAtWarps = 4;       // consumer warps, 16 keys of each tile each
 constexpr int kAtThreads = 32 * (kAtWarps + 1);
+constexpr int kAtVisit = 1;      // tiles that an own unit counts beyond its own
 constexpr int kAtSmallRows = 16;  // rows of a batch whose prefix needs no tcgen05 tile
 
 // The part of the keys that sequence b's row sees, as 64-key tiles.
@@ -129,7 +134,8 @@ template <bool kPre>
 struct AtWalk {
   const AttnK &a;
   const int32_t *cum;  // shared memory copy (own)
-  long long t, end;
+  static constexpr int kV = kPre ? 0 : kAtVisit;
+  long long t, end;    // places in the list: kV in front of a unit's tiles
   int b, h, unit;      // current unit (prefix: b = row block)
   int in, n;           // tile in the unit, its tiles
   Span s;
@@ -150,12 +156,14 @@ struct AtWalk {
         else hi = mid;
       }
       b = lo;
-      n = cum[b + 1] - cum[b];
+      const int len = cum[b + 1] - cum[b];
       const long long r = t - (long long)a.H * cum[b];
-      h = (int)(r / n);
-      in = (int)(r - (long long)h * n);
+      h = (int)(r / len);
+      n = len - kV;
+      in = (int)(r - (long long)h * len) - kV;
       unit = b * a.H + h;
       s = seq_span(a, b);
+      if (in < 0) t -= in, in = 0;
     }
   }
   FLINT_DEV bool done() const { return t >= end; }
@@ -178,18 +186,27 @@ struct AtWalk {
     ++t, ++in;
     if (t >= end) return true;
     if (in < n) return false;
-    in = 0;
+    in = 0, t += kV;
+    if (t >= end) return true;
     ++unit;
     if (++h == a.H) {
       h = 0, ++b;
       if (!kPre) {
         while (cum[b + 1] == cum[b]) ++b, unit += a.H;
-        n = cum[b + 1] - cum[b];
+        n = cum[b + 1] - cum[b] - kV;
         s = seq_span(a, b);
       }
     }
     return true;
   }
+};
+
+// Where the warps' outputs of a unit are added: kCopies warps at once, rows
+// padded by four words (a warp's stores go to 32 different banks).
+template <int kD, int kNT>
+struct AtJoin {
+  static constexpr int kPitch = kD + 4, kCopies = 2 / kNT;
+  static constexpr int kCopy = 8 * kNT * kPitch, kFloats = kCopies * kCopy;
 };
 
 // kRows = 8 kNT query rows a unit
@@ -203,8 +220,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   extern __shared__ unsigned char smraw[];
   unsigned char *sm = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
-  float *osum = reinterpret_cast<float *>(sm + (size_t)kSt * 2 * Tile::kBytes);  // [kRows][kD]
-  float2 *wml = reinterpret_cast<float2 *>(osum + kRows * kD);                   // [warps][kRows]
+  using Join = AtJoin<kD, kNT>;
+  float *osum = reinterpret_cast<float *>(sm + (size_t)kSt * 2 * Tile::kBytes);
+  float2 *wml = reinterpret_cast<float2 *>(osum + Join::kFloats);                // [warps][kRows]
   int32_t *cum = reinterpret_cast<int32_t *>(wml + kAtWarps * kRows);            // [B + 1]
   __shared__ __align__(8) uint64_t full[kSt], empty[kSt];
   __shared__ int s_fail, s_scan[kAtWarps + 1];
@@ -232,6 +250,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       if (b < a.B) {
         const Span s = seq_span(a, b);
         v = s.p_tiles + s.o_tiles;
+        if (v) v += kAtVisit;
       }
       int inc = v;
 #pragma unroll
@@ -267,34 +286,37 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     const int boxes = per * Tile::kHalves;      // of K; V as many
     int issued = 0;
     bool ok = true;
+    const int is_v = lane >= boxes, box = is_v ? lane - boxes : lane;
+    const int half = box / per, x = box % per;  // 2 boxes <= 32
     for (uint32_t it = 0; !w.done(); ++it) {
       const int st = it % kSt;
       const AtTileDesc d = w.tile();
-      if (it >= kSt)
-        ok = __all_sync(0xffffffffu, mbar_wait_sleep(&empty[st], ((it / kSt) - 1) & 1));
-      if (!ok) break;
       // boxes that hold a visible key
       const int k_lo = max(d.lo, d.key0), k_hi = min(d.hi, d.key0 + kAtKeys);
       const int b_lo = (k_lo - d.key0) / a.box_rows;
       const int b_hi = ceil_div(k_hi - d.key0, a.box_rows);
+      const bool mine = lane < 2 * boxes && x >= b_lo && x < b_hi;
+      // the page's number arrives while the stage is waited for
+      int page = 0, row = 0;
+      if (mine) {
+        const int key = d.key0 + x * a.box_rows, pg = key / a.page_size;
+        row = key - pg * a.page_size;
+        page = d.prefix ? a.prefix_pages[pg] : a.table[(size_t)d.b * a.max_pages + pg];
+      }
+      if (it >= kSt)
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(&empty[st], ((it / kSt) - 1) & 1));
+      if (!ok) break;
       if (lane == 0)
         mbar_expect_tx(&full[st],
                        (uint32_t)((b_hi - b_lo) * a.box_rows * Tile::kRow * 2));
       __syncwarp();
-      unsigned char *kt = sm + (size_t)st * 2 * Tile::kBytes;
-      for (int i = lane; i < 2 * boxes; i += 32) {
-        const int is_v = i >= boxes, j = is_v ? i - boxes : i;
-        const int half = j / per, x = j % per;
-        if (x < b_lo || x >= b_hi) continue;
-        const int key = d.key0 + x * a.box_rows;
-        const int pg = key / a.page_size, row = key - pg * a.page_size;
-        int page = d.prefix ? a.prefix_pages[pg] : a.table[(size_t)d.b * a.max_pages + pg];
+      if (mine) {
         if ((unsigned)page >= (unsigned)a.num_pages) {
           set_status(a.status, kStatusDevice);
           page = a.num_pages;  // outside the tensor: the copy fills zeros
         }
-        tma_load_4d(kt + (is_v ? Tile::kBytes : 0) + half * Tile::kHalfBytes +
-                        x * a.box_rows * Tile::kHalfRow,
+        tma_load_4d(sm + (size_t)st * 2 * Tile::kBytes + (is_v ? Tile::kBytes : 0) +
+                        half * Tile::kHalfBytes + x * a.box_rows * Tile::kHalfRow,
                     is_v ? &tmV : &tmK, half * (Tile::kHalfRow / (kF8 ? 1 : 2)), row, d.h, page,
                     &full[st]);
       }
@@ -315,77 +337,86 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     // the same with rows and chunks swapped (bf16 V)
     const int rv = k0 + (lane & 7) + (lane >> 4) * 8, cv = (lane >> 3) & 1;
     bool ok = true;
-    uint32_t qf[kNT][kKs][2];
     float rs[kNT][2];     // score factors of rows 2 t4, 2 t4 + 1
     float m[kNT][2], l[kNT][2];
     float o[kKs][kNT][4];
-    bool begin = true;
+    // the query rows of unit (b, h), as they are in memory; this lane's column
+    // is row g of each eight
+    uint32_t qr[kNT][kKs][2];
+    auto load_q = [&](int b, int h) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const int r = 8 * nt + g;
+        const int R = kPre ? b * kRows + r : b * a.G + r;
+        const bool valid = kPre ? R < a.B * a.G : r < a.G;
+        const int sb = valid ? R / a.G : 0, sg = valid ? R - sb * a.G : 0;
+        const uint16_t *p = a.q + (int64_t)sb * a.q_stride + (int64_t)(h * a.G + sg) * kD;
+#pragma unroll
+        for (int k = 0; k < kKs; ++k) {
+          if (kF8) {
+            const uint2 v = valid ? *reinterpret_cast<const uint2 *>(p + 16 * k + 4 * t4)
+                                  : make_uint2(0, 0);
+            qr[nt][k][0] = v.x, qr[nt][k][1] = v.y;
+          } else {
+            qr[nt][k][0] = valid ? *reinterpret_cast<const uint32_t *>(p + 16 * k + 2 * t4) : 0u;
+            qr[nt][k][1] =
+                valid ? *reinterpret_cast<const uint32_t *>(p + 16 * k + 2 * t4 + 8) : 0u;
+          }
+        }
+      }
+    };
+    auto begin_unit = [&](int h) {
+      const float ks = kF8 && a.k_scale ? a.k_scale[h] : 1.f;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        float fac = a.scale2 * ks;
+        if (kF8) {
+          // fp16 operands: the row times a power of two that puts its
+          // largest element in [2^14, 2^15) (exact for elements down to
+          // 2^-28 of it), divided out of the scores
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < kKs; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              top = max(top, max(qr[nt][k][i] & 0x7fffu, (qr[nt][k][i] >> 16) & 0x7fffu));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // exponent field e of the largest: times 2^(141 - e); two factors
+          // keep each a normal number
+          const int e = min(max((int)(top >> 7), 1), 254);
+          const int sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
+          const float f1 = __uint_as_float((uint32_t)(127 + s1) << 23);
+          const float f2 = __uint_as_float((uint32_t)(127 + s2) << 23);
+          fac *= __uint_as_float((uint32_t)(127 - s1) << 23);
+          fac *= __uint_as_float((uint32_t)(127 - s2) << 23);
+#pragma unroll
+          for (int k = 0; k < kKs; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              qr[nt][k][i] = pack_f16(__uint_as_float(qr[nt][k][i] << 16) * f1 * f2,
+                                      __uint_as_float(qr[nt][k][i] & 0xffff0000u) * f1 * f2);
+        }
+        // fac belongs to row g; this lane's scores are of rows 2 t4, 2 t4 + 1
+        rs[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * t4);
+        rs[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * t4 + 4);
+        m[nt][0] = m[nt][1] = -__int_as_float(0x7f800000);
+        l[nt][0] = l[nt][1] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kKs; ++k)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+          o[k][nt][0] = o[k][nt][1] = o[k][nt][2] = o[k][nt][3] = 0.f;
+    };
+    if (!w.done()) {
+      load_q(w.b, w.h);
+      begin_unit(w.h);
+    }
     for (uint32_t it = 0; !w.done(); ++it) {
       const int st = it % kSt;
       const AtTileDesc d = w.tile();
       const int unit = w.unit;
-      if (begin) {
-        const float ks = kF8 && a.k_scale ? a.k_scale[d.h] : 1.f;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          // query row of this lane's column g
-          const int r = 8 * nt + g;
-          const int R = kPre ? d.b * kRows + r : d.b * a.G + r;
-          const bool valid = kPre ? R < a.B * a.G : r < a.G;
-          const int sb = R / a.G, sg = R - sb * a.G;
-          const uint16_t *qr = a.q + (int64_t)sb * a.q_stride + (int64_t)(d.h * a.G + sg) * kD;
-          float fac = a.scale2 * ks;
-          if (kF8) {
-            // fp16 operands: the row times a power of two that puts its
-            // largest element in [2^14, 2^15) (exact for elements down to
-            // 2^-28 of it), divided out of the scores
-            uint2 v[kKs];
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < kKs; ++k) {
-              v[k] = valid ? *reinterpret_cast<const uint2 *>(qr + 16 * k + 4 * t4)
-                           : make_uint2(0, 0);
-              top = max(max(top, v[k].x & 0x7fffu), max((v[k].x >> 16) & 0x7fffu, v[k].y & 0x7fffu));
-              top = max(top, (v[k].y >> 16) & 0x7fffu);
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // exponent field e of the largest: times 2^(141 - e); two factors
-            // keep each a normal number
-            const int e = min(max((int)(top >> 7), 1), 254);
-            const int sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
-            const float f1 = __uint_as_float((uint32_t)(127 + s1) << 23);
-            const float f2 = __uint_as_float((uint32_t)(127 + s2) << 23);
-            fac *= __uint_as_float((uint32_t)(127 - s1) << 23);
-            fac *= __uint_as_float((uint32_t)(127 - s2) << 23);
-#pragma unroll
-            for (int k = 0; k < kKs; ++k) {
-              qf[nt][k][0] = pack_f16(__uint_as_float(v[k].x << 16) * f1 * f2,
-                                      __uint_as_float(v[k].x & 0xffff0000u) * f1 * f2);
-              qf[nt][k][1] = pack_f16(__uint_as_float(v[k].y << 16) * f1 * f2,
-                                      __uint_as_float(v[k].y & 0xffff0000u) * f1 * f2);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < kKs; ++k) {
-              qf[nt][k][0] = valid ? *reinterpret_cast<const uint32_t *>(qr + 16 * k + 2 * t4) : 0u;
-              qf[nt][k][1] =
-                  valid ? *reinterpret_cast<const uint32_t *>(qr + 16 * k + 2 * t4 + 8) : 0u;
-            }
-          }
-          // fac belongs to row g; this lane's scores are of rows 2 t4, 2 t4 + 1
-          rs[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * t4);
-          rs[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * t4 + 4);
-          m[nt][0] = m[nt][1] = -__int_as_float(0x7f800000);
-          l[nt][0] = l[nt][1] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < kKs; ++k)
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-            o[k][nt][0] = o[k][nt][1] = o[k][nt][2] = o[k][nt][3] = 0.f;
-        begin = false;
-      }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (it / kSt) & 1));
       const int lo = d.lo - d.key0 - k0, hi = d.hi - d.key0 - k0;  // visible of this warp's 16
       if (ok && lo < 16 && hi > 0) {
@@ -415,7 +446,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
             ldsm4(f, ka + Tile::at(rk, 2 * k + ck));
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma_bf16_16816(sc[nt], f[0], f[1], f[2], f[3], qf[nt][k][0], qf[nt][k][1]);
+              mma_bf16_16816(sc[nt], f[0], f[1], f[2], f[3], qr[nt][k][0], qr[nt][k][1]);
           }
         } else {
 #pragma unroll
@@ -429,7 +460,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
               const uint32_t a1 = e4m3x2_to_f16x2(y), a3 = e4m3x2_to_f16x2(y >> 16);
 #pragma unroll
               for (int nt = 0; nt < kNT; ++nt)
-                mma_f16_16816(sc[nt], a0, a1, a2, a3, qf[nt][k + j][0], qf[nt][k + j][1]);
+                mma_f16_16816(sc[nt], a0, a1, a2, a3, qr[nt][k + j][0], qr[nt][k + j][1]);
             }
           }
         }
@@ -521,7 +552,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
       if (w.next()) {
-        // the unit's part is complete: join the warps and write it
+        // the unit's part is complete: join the warps and write it, while the
+        // next unit's query rows arrive
+        if (!w.done()) load_q(w.b, w.h);
         float fac[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
@@ -542,8 +575,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
             fac[nt][i] = at_ex2(m[nt][i] - (top == -__int_as_float(0x7f800000) ? 0.f : top));
           }
         const size_t slot = (size_t)unit + c;
-        for (int x = 0; x < kAtWarps; ++x) {
-          if (warp == x) {
+        for (int x = 0; x < kAtWarps / Join::kCopies; ++x) {
+          if (warp / Join::kCopies == x) {
+            float *mine = osum + warp % Join::kCopies * Join::kCopy;
 #pragma unroll
             for (int k = 0; k < kKs; ++k)
 #pragma unroll
@@ -553,15 +587,23 @@ __global__ void __launch_bounds__(kAtThreads, 2)
                   const int r = 8 * nt + 2 * t4 + (i & 1);
                   const int e = kF8 ? 16 * k + 2 * g + (i >> 1) : 16 * k + g + 8 * (i >> 1);
                   const float v = o[k][nt][i] * fac[nt][i & 1];
-                  float *dst = &osum[r * kD + e];
+                  float *dst = &mine[r * Join::kPitch + e];
                   *dst = x == 0 ? v : *dst + v;
                 }
           }
           asm volatile("bar.sync 1, 128;" ::: "memory");
         }
         float *op = (kPre ? a.o_pre : a.o_own) + slot * kRows * kD;
-        for (int i = tid; i < kRows * kD / 4; i += 32 * kAtWarps)
-          reinterpret_cast<float4 *>(op)[i] = reinterpret_cast<const float4 *>(osum)[i];
+        const int live = kPre ? kRows : min(a.G, kRows);
+        for (int i = tid; i < live * kD / 4; i += 32 * kAtWarps) {
+          const int at = i / (kD / 4) * Join::kPitch + 4 * (i % (kD / 4));
+          float4 v = *reinterpret_cast<const float4 *>(osum + at);
+          if (Join::kCopies == 2) {
+            const float4 y = *reinterpret_cast<const float4 *>(osum + Join::kCopy + at);
+            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+          }
+          reinterpret_cast<float4 *>(op)[i] = v;
+        }
         if (tid < kRows) {
           float top = wml[tid].x, sum = 0.f;
           for (int x = 1; x < kAtWarps; ++x) top = fmaxf(top, wml[x * kRows + tid].x);
@@ -571,7 +613,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
           (kPre ? a.ml_pre : a.ml_own)[slot * kRows + tid] = make_float2(top, sum);
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        begin = true;
+        if (!w.done()) begin_unit(w.h);
       }
     }
     if (!ok) s_fail = 1;
@@ -582,23 +624,27 @@ __global__ void __launch_bounds__(kAtThreads, 2)
 }
 
 // ------------------------------------------------------------------ joining the parts
-// One warp a query row: the parts' maxima and the sink give the base, then the
-// parts' sums and outputs are added in list order (prefix first).
-template <int kD>
+// kWarps warps a query row: the parts' maxima and the sink give the base; each
+// warp adds every kWarps-th part's sums and outputs in list order (prefix
+// first), and the warps' are added in order.  One warp where the rows fill the
+// GPU; eight where they do not and a row has many parts (8 sequences of up to
+// 131,072 keys, 37 parts a row: 12 us with one, the loads' latency).
+template <int kD, int kWarps>
 __global__ void __launch_bounds__(256)
     k_attn_combine(const __grid_constant__ AttnK a, int own_rows, int grid_own) {
+  __shared__ float2 part[8][kD / 2 + 1];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % kWarps;
+  const int row = (blockIdx.x * 8 + warp) / kWarps;
   const int q_heads = a.G * a.H;
-  if (row >= a.B * q_heads) return;
+  if (kWarps < 8 && row >= a.B * q_heads) return;
   const int b = row / q_heads, head = row % q_heads, h = head / a.G, g = head % a.G;
   const float kNegInf = -__int_as_float(0x7f800000);
   const bool has = a.lens[b] >= 0;
   // parts of this row: prefix slots [p0, p1), own slots [s0, s1)
   int p0 = 0, p1 = 0, s0 = 0, s1 = 0, pr = 0;
-  if (has && a.window == 0 && a.prefix_len > 0) {
+  if (has && a.behind_prefix) {
     const int R = b * a.G + g, blk = R / a.pre_rows;
     pr = R % a.pre_rows;
     const int n = ceil_div(a.prefix_len, a.pre_keys), u = blk * a.H + h;
@@ -612,7 +658,7 @@ __global__ void __launch_bounds__(256)
     const long long tiles = (long long)a.H * a.cum[a.B];
     const int ctas = list_ctas(tiles, grid_own), u = b * a.H + h;
     const long long t = (long long)a.H * c0 + (long long)h * n;
-    s0 = u + list_cta(tiles, ctas, t);
+    s0 = u + list_cta(tiles, ctas, t + kAtVisit);
     s1 = u + list_cta(tiles, ctas, t + n - 1) + 1;
   }
   const float sink = a.sinks ? a.sinks[head] * kLog2e : kNegInf;
@@ -628,7 +674,7 @@ __global__ void __launch_bounds__(256)
   float acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-  float sum = at_ex2(sink - base);
+  float sum = w == 0 ? at_ex2(sink - base) : 0.f;
   auto add = [&](const float2 *mlp, const float *op) {
     const float m = ld_cg_f32(&mlp->x), l = ld_cg_f32(&mlp->y);
     const float f = at_ex2(m - base);
@@ -642,11 +688,26 @@ __global__ void __launch_bounds__(256)
     }
   };
 #pragma unroll 4
-  for (int i = p0; i < p1; ++i)
+  for (int i = p0 + w; i < p1; i += kWarps)
     add(a.ml_pre + (size_t)i * a.pre_rows + pr, a.o_pre + ((size_t)i * a.pre_rows + pr) * kD);
 #pragma unroll 4
-  for (int i = s0; i < s1; ++i)
+  for (int i = s0 + w; i < s1; i += kWarps)
     add(a.ml_own + (size_t)i * own_rows + g, a.o_own + ((size_t)i * own_rows + g) * kD);
+  if (kWarps > 1) {
+#pragma unroll
+    for (int i = 0; i < kV; i += 2) part[warp][16 * i + lane] = make_float2(acc[i], acc[i + 1]);
+    if (lane == 0) part[warp][16 * kV].x = sum;
+    __syncthreads();
+    if (w) return;
+    for (int x = 1; x < kWarps; ++x) {
+#pragma unroll
+      for (int i = 0; i < kV; i += 2) {
+        const float2 y = part[warp + x][16 * i + lane];
+        acc[i] += y.x, acc[i + 1] += y.y;
+      }
+      sum += part[warp + x][16 * kV].x;
+    }
+  }
   const float vs = a.v_scale ? a.v_scale[h] : 1.f;
   const float inv = sum == 0.f ? 0.f : vs / sum;
   uint16_t *dst = a.out + (int64_t)b * a.out_stride + (int64_t)head * kD;
@@ -730,7 +791,7 @@ cudaError_t launch_parts(const CUtensorMap &k, const CUtensorMap &v, const AttnK
                          cudaStream_t st) {
   using Tile = AtTile<kD, kF8>;
   const size_t smem = 1024 + (size_t)Tile::kStages * 2 * Tile::kBytes +
-                      sizeof(float) * 8 * kNT * kD + sizeof(float2) * kAtWarps * 8 * kNT +
+                      sizeof(float) * AtJoin<kD, kNT>::kFloats + sizeof(float2) * kAtWarps * 8 * kNT +
                       (kPre ? 0 : sizeof(int32_t) * ((size_t)a.B + 1));
   return at_launch(k_attn_parts<kD, kF8, kNT, kPre>, grid, kAtThreads, smem, st, k, v, a);
 }
@@ -792,8 +853,9 @@ cudaError_t launch_attn_as(const flint_kv_cache &c, const CUtensorMap &k, const 
                : launch_parts<kD, kF8, 2, false>(k, v, a, wide, st);
   if (e != cudaSuccess) return e;
   note_step("attention combine launch");
-  return at_launch(k_attn_combine<kD>, ceil_div(rows * a.H, 8), 256, 0, st, a, a.G <= 8 ? 8 : 16,
-                   wide);
+  const int own_rows = a.G <= 8 ? 8 : 16, all = rows * a.H;
+  if (all <= 8 * sms) return at_launch(k_attn_combine<kD, 8>, all, 256, 0, st, a, own_rows, wide);
+  return at_launch(k_attn_combine<kD, 1>, ceil_div(all, 8), 256, 0, st, a, own_rows, wide);
 }
 
 }  // namespace
