@@ -49,19 +49,37 @@ struct PreCfg {
   static_assert(256 * kRegSoft + (kThreads - 256) * kRegCtl <= kThreads * kRegLaunch, "registers");
 };
 
-// D (tensor memory, 128 lanes) += A (tensor memory, 16-bit pairs) B (shared memory)
-FLINT_DEV void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, "
-      "%3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accum));
+// One lane of a converged warp, the same one each time.  Unlike `lane == 0`
+// it lets the products below be issued from uniform registers.
+FLINT_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+  return p != 0;
 }
-// Shared-memory descriptor of an operand whose rows are its K dimension, in
-// 128-byte swizzle: 8-row groups 1,024 bytes apart, 64-element pieces of a
-// row `piece` bytes apart.
-FLINT_DEV uint64_t sw128_mn_desc(uint32_t saddr, uint32_t piece) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(piece >> 4) << 16) | (64ull << 32) |
-         (1ull << 46) | (2ull << 61);
+// The upper halves of the two operand descriptors (sw128_desc, sw128_mn_desc)
+// are one constant; the lower ones are an address (and a stride) that the
+// steps of a product advance.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+// D (tensor memory, 128 lanes) += A B, both from shared memory
+FLINT_DEV void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 x, {%1, %5};\n"
+      "mov.b64 y, {%2, %5};\ntcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accum), "n"(kDescHi));
+}
+// the same with A from tensor memory (16-bit pairs)
+FLINT_DEV void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 y, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accum), "n"(kDescHi));
+}
+// Lower half of a K-major operand's descriptor: its address.  And of an
+// operand whose rows are its K dimension: 8-row groups 1,024 bytes apart (the
+// upper half), 64-element pieces of a row kAtom bytes apart.
+FLINT_DEV uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+FLINT_DEV uint32_t desc_mn(uint32_t saddr, uint32_t piece) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((piece >> 4) << 16);
 }
 // keeps uses of loaded registers behind the wait
 FLINT_DEV void pin32(uint32_t *v) {
@@ -128,7 +146,8 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
   __shared__ __align__(8) uint64_t sfull[2], pready[2], ofull[2], qready[2], done;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in the warp
   if (tid == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&full[s], kF8 ? 4 : 1);
@@ -220,6 +239,8 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
       uint32_t np[2] = {0, 0};     // P tiles taken of block x
       uint32_t nq[2] = {0, 0};     // units begun by block x
       bool ok = true;
+      const bool leader = elect_one();
+      const uint32_t q_a = smem_addr(sm), slots_a = smem_addr(slots);
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
       };
@@ -230,12 +251,14 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
         const uint32_t sv = (2 * i + 1) % C::kSlots;
         if (!ok) return;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t va = smem_addr(slots + sv * C::kTile);
+        if (leader) {
+          const uint32_t vd = desc_mn(slots_a + sv * C::kTile, C::kAtom);
           const int steps = (keys + 15) / 16;
-          for (int q = 0; q < steps; ++q)
-            umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * q,
-                    sw128_mn_desc(va + 2048 * q, C::kAtom), kDescO, !first || q > 0);
+#pragma unroll
+          for (int q = 0; q < kPkKeys / 16; ++q)
+            if (q < steps)
+              umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * q, vd + 128 * q, kDescO,
+                      !first || q > 0);
         }
         __syncwarp();
       };
@@ -268,13 +291,12 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
             if (j > r.j0) product_o(x, k - 1, kPkKeys, j - 1 == r.j0);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-              const uint32_t qa = smem_addr(sm + x * C::kTile), ka = smem_addr(slots + sk * C::kTile);
+            if (leader) {
+              const uint32_t qd = desc_k(q_a + x * C::kTile), kd = desc_k(slots_a + sk * C::kTile);
 #pragma unroll
               for (int q = 0; q < kD / 16; ++q) {
-                const uint32_t off = (q >> 2) * C::kAtom + (q & 3) * 32;
-                umma_bf16_ss(tmem + 128 * x, sw128_desc(qa + off), sw128_desc(ka + off), kDescS,
-                             q > 0);
+                const uint32_t off = ((q >> 2) * C::kAtom + (q & 3) * 32) >> 4;
+                umma_ss(tmem + 128 * x, qd + off, kd + off, kDescS, q > 0);
               }
               umma_commit1(&sfull[x]);
               if (x + 1 == nb) {
@@ -289,7 +311,7 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
         if (ok) wait_v(k - 1, last_keys);
         for (int x = 0; x < nb && ok; ++x) {
           product_o(x, k - 1, last_keys, r.j1 - r.j0 == 1);
-          if (ok && lane == 0) {
+          if (ok && leader) {
             umma_commit1(&ofull[x]);
             if (x + 1 == nb) umma_commit1(&empty[(2 * k - 1) % C::kSlots]);
           }
@@ -297,7 +319,7 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
         }
       }
       if (!ok) s_fail = 1;
-      if (lane == 0) umma_commit1(&done);  // every product completes before tensor memory is freed
+      if (leader) umma_commit1(&done);  // every product completes before tensor memory is freed
       __syncwarp();
       if (!mbar_wait(&done, 0)) s_fail = 1;
     } else if (kF8 && warp >= 12) {
@@ -477,20 +499,30 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
       float l0, l1, l;
       unpair2(add2(l2a, l2b), l0, l1);
       l = l0 + l1;
-      const size_t at = ((size_t)r.unit + blockIdx.x) * a.pre_rows + 128 * x + row;
-      if (valid) a.ml_pre[at] = make_float2(m, l);
+      const size_t at = ((size_t)r.unit + blockIdx.x) * a.pre_rows + 128 * x + 32 * (warp & 3);
+      if (valid) a.ml_pre[at + lane] = make_float2(m, l);
+      // through this warp's rows of Q (no product reads them any more), so
+      // that a store covers four rows' whole 128-byte lines
+      unsigned char *stage = sm + x * C::kTile + 32 * (warp & 3) * 128;
 #pragma unroll 1
       for (int c = 0; c < kD / 32; ++c) {
         uint32_t o[32];
         tmem_ld32_async(to + 32 * c, o);
         tmem_wait_ld();
         pin32(o);
-        if (valid) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.o_pre + at * kD + 32 * c);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+          if (R0 + 32 * (warp & 3) + rr < rows)
+            *reinterpret_cast<uint4 *>(a.o_pre + (at + rr) * kD + 32 * c + 4 * ch) =
+                *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
         }
+        __syncwarp();
       }
     }
     if (!ok) s_fail = 1;
