@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
   unsigned char *slots = sm + C::kQ, *raw = slots + C::kSlots * C::kTile;
   __shared__ __align__(8) uint64_t full[C::kSlots], empty[C::kSlots];
   __shared__ __align__(8) uint64_t rfull[kF8 ? C::kRaw : 1], rempty[kF8 ? C::kRaw : 1];
-  __shared__ __align__(8) uint64_t sfull[2], pready[2], ofull[2], qready[2], done;
+  __shared__ __align__(8) uint64_t sfull[2], pready[2][2], ofull[2], qready[2], done;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sfull[x], 1);
-      mbar_init(&pready[x], 4);
+      mbar_init(&pready[x][0], 4);
+      mbar_init(&pready[x][1], 4);
       mbar_init(&ofull[x], 1);
       mbar_init(&qready[x], 4);
     }
@@ -246,21 +247,24 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
       };
       // O_x (+)= P V of tile i, whose key count is `keys`
       auto product_o = [&](int x, uint32_t i, int keys, bool first) {
-        wait(&pready[x], np[x] & 1);
-        ++np[x];
         const uint32_t sv = (2 * i + 1) % C::kSlots;
-        if (!ok) return;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t vd = desc_mn(slots_a + sv * C::kTile, C::kAtom);
-          const int steps = (keys + 15) / 16;
+        const uint32_t vd = desc_mn(slots_a + sv * C::kTile, C::kAtom);
+        const int steps = (keys + 15) / 16;
 #pragma unroll
-          for (int q = 0; q < kPkKeys / 16; ++q)
-            if (q < steps)
-              umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * q, vd + 128 * q, kDescO,
-                      !first || q > 0);
+        for (int hf = 0; hf < 2; ++hf) {
+          wait(&pready[x][hf], np[x] & 1);
+          if (!ok) return;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int q = 4 * hf; q < 4 * hf + 4; ++q)
+              if (q < steps)
+                umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * q, vd + 128 * q, kDescO,
+                        !first || q > 0);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        ++np[x];
       };
       // V of tile i is there; rows behind the last key of its last 16 hold
       // what the page holds, which must not reach the sums even times 0
@@ -471,6 +475,7 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
           }
         }
         const float base = m == kNegInf ? 0.f : m;
+        // in halves: the products of the first begin under the second's exponentials
         const uint64_t fac2 = pair2(fac, fac), nb2 = pair2(-base, -base);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -486,11 +491,11 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
             p[i] = kF8 ? pk_f16(p0, p1) : pack_bf16(p0, p1);
           }
           tmem_st32(ts + 32 * c, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pready[x][c]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[x]);
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&ofull[x], nu & 1));
       ++nu;
