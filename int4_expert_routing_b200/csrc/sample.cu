@@ -3,27 +3,33 @@
 //
 // No sort of the vocabulary: the kept set is "everything from a cut on" in
 // the order (logit down, index up), so only the cut is searched.  A cluster
-// of CTAs takes a row and holds it in shared memory, read from HBM once:
+// of CTAs takes a row and holds it in shared memory, read from HBM once.  An
+// element's place in the order is one 64-bit key (logit, then index), so that
+// equal logits need no case of their own.
+//
+// Few kept tokens (top-k of up to kSmShort, greedy rows): each CTA finds a
+// threshold that at least k of its threads' largest logits reach, and hands
+// the elements above it (k and a few) to one CTA, which puts them in order
+// and does the rest with block barriers alone.
+//
+// Otherwise:
 //   1. the largest logit M;
 //   2. a histogram over d = (M - z) log2(e) / temperature in steps of 1/32:
 //      each bin's count and mass.  The mass is summed in integers: within a
 //      bin 2^-d is 2^(-bin/32) (1 - e) with e < 0.0215, and the sum of e in
-//      units of 2^-22 fits 32 bits for the 2^15 elements of a CTA and does not depend on
-//      the order of the atomics;
-//   3. the bins' running count and mass name the bin a cut falls in; its
-//      elements (a few of them) are gathered into one CTA and put in order.
-//      A bin with too many is first halved by key, and equal logits are cut
-//      by index;
-//   4. the kept mass in index order (fp64, fixed order), and the token whose
-//      running mass passes u times the total.
+//      units of 2^-22 fits 32 bits for the 2^15 elements of a CTA and does not
+//      depend on the order of the atomics;
+//   3. the bins' running count and mass name the bin a cut falls in.  Its
+//      elements are gathered into one CTA, which narrows them down by 512 bins
+//      of the key and orders the last few.  More than fit there (flat rows,
+//      equal logits) are narrowed down by bins of the key in the cluster first;
+//   4. the kept mass in index order (pieces of 128 elements in fp32, their sums
+//      in fp64, fixed order), and the token whose running mass passes u times
+//      the total.
 // Every sum has a fixed order or is an integer, so a row's result does not
 // vary between runs, nor with the other rows.
-#include <cooperative_groups.h>
-
 #include "common.cuh"
 #include "internal.h"
-
-namespace cg = cooperative_groups;
 
 namespace flint {
 
@@ -31,28 +37,44 @@ constexpr int kSmThreads = 512;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBins = 1024;       // steps of 1/32 in log2 units: d < 32
 constexpr float kSmSteps = 32.f;
-constexpr int kSmList = 512;        // elements put in order at once
+constexpr int kSmList = 2048;       // elements gathered in one CTA
+constexpr int kSmOrder = 512;       // elements put in order at once
+constexpr int kSmShort = 256;       // largest k of the short path
 constexpr int kSmMaxCluster = 8;
-constexpr float kEpsUnit = 4194304.f;  // 2^22
+constexpr int kSmChunk = 128;       // elements of a sum of the last step
+constexpr int kSmChunks = FLINT_MAX_VOCAB / kSmMaxCluster / kSmChunk + 2;
+constexpr float kEpsUnit = 4194304.f;          // 2^22
+constexpr float kFarUnit = 281474976710656.f;  // 2^48
+constexpr uint32_t kNoneKey = 0x007fffffu;     // -inf: never chosen
+
+typedef unsigned long long u64;
 
 struct SampleShared {
-  uint32_t cnt[kSmBins], eps[kSmBins];  // this CTA's bins
-  uint32_t tcnt[kSmBins];               // the cluster's
-  double tmass[kSmBins];
-  unsigned long long list[kSmList], sorted[kSmList];
+  union {
+    struct {
+      uint32_t cnt[kSmBins], eps[kSmBins];  // this CTA's bins
+      uint32_t tcnt[kSmBins];               // the cluster's
+      double tmass[kSmBins];
+    };
+    u64 list[kSmList];
+  };
+  u64 sorted[kSmOrder], mine[kSmOrder];
+  uint32_t scnt[kSmThreads], seps[kSmThreads];
   // one exchange between the CTAs uses one of two sets of slots, in turn
   struct {
-    unsigned long long a;
+    u64 a;
     double b;
   } slot[2][kSmMaxCluster];
-  unsigned long long red_a[kSmWarps];
+  uint32_t red_c[kSmWarps];
+  u64 red_a[kSmWarps];
   double red_b[kSmWarps];
-  double wsum[kSmWarps];
-  double lmass[kSmList];
-  unsigned long long res_key;
+  float chunk[kSmChunks];
+  u64 res_key;
   double res_mass;
-  uint32_t list_n;
+  uint32_t list_n, mine_n;
   int found;
+  uint32_t at_n, at_above;
+  double at_mass;
 };
 
 FLINT_DEV float ex2(float x) {
@@ -61,13 +83,18 @@ FLINT_DEV float ex2(float x) {
   return y;
 }
 
-struct Sum2 {
-  unsigned long long a;
-  double b;
-};
+// (z, index) as one number: larger = earlier in the order.  -0 counts as +0.
+FLINT_DEV uint32_t zkey(float z) { return float_key(z + 0.f); }
+FLINT_DEV float key_z(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+FLINT_DEV u64 order_key(float z, int index) {
+  return ((u64)zkey(z) << 32) | (0xffffffffu - (uint32_t)index);
+}
+FLINT_DEV int key_index(u64 k) { return (int)(0xffffffffu - (uint32_t)k); }
 
 // A row's view in one CTA: z[0 .. 4 n4) with index0 the row index of z[0]
-// (it may start up to 3 elements early; those hold -inf).
+// (it may start up to 3 elements early; those hold -inf, as NaN ones do).
 struct RowPart {
   const float4 *z;
   int n4;
@@ -78,84 +105,123 @@ template <typename F>
 FLINT_DEV void for_elements(const RowPart &r, F f) {
   for (int i = threadIdx.x; i < r.n4; i += kSmThreads) {
     const float4 v = r.z[i];
-    f(v.x, 4 * i);
-    f(v.y, 4 * i + 1);
-    f(v.z, 4 * i + 2);
-    f(v.w, 4 * i + 3);
+    f(v.x, r.index0 + 4 * i);
+    f(v.y, r.index0 + 4 * i + 1);
+    f(v.z, r.index0 + 4 * i + 2);
+    f(v.w, r.index0 + 4 * i + 3);
   }
-}
-
-// (z, index) as one number: larger = earlier in the order.  -0 counts as +0.
-FLINT_DEV uint32_t zkey(float z) { return float_key(z + 0.f); }
-FLINT_DEV float key_z(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
 struct Dist {
   float M, c;
-  // log2 of p(max) / p(z), >= 0; +inf where p = 0 (NaN, -inf)
+  // log2 of p(max) / p(z), >= 0; +inf where p = 0 (-inf)
   FLINT_DEV float operator()(float z) const {
     const float d = (M - z) * c;
     return z == M ? 0.f : (d >= 0.f ? d : __int_as_float(0x7f800000));
   }
+  FLINT_DEV float p(float z) const { return ex2(-(*this)(z)); }
   FLINT_DEV int bin(float z) const {
     const float d = (*this)(z);
     return d < (float)kSmBins / kSmSteps ? (int)(d * kSmSteps)
                                          : (z > -__int_as_float(0x7f800000) ? kSmBins : -1);
   }
+  // what an element of bin b adds to the bin's integer, and the mass that a
+  // count and such a sum stand for: the shortfall from the bin's first value,
+  // or the value itself behind the bins
+  FLINT_DEV uint32_t units(float z, int b) const {
+    const float d = (*this)(z);
+    if (b == kSmBins) return (uint32_t)(ex2(-d) * kFarUnit + 0.5f);
+    const float e = 1.f - ex2((float)b * (1.f / kSmSteps) - d);
+    return (uint32_t)(fmaxf(e, 0.f) * kEpsUnit + 0.5f);
+  }
+  FLINT_DEV static double mass(u64 n, u64 units, int b) {
+    if (b == kSmBins) return (double)units / kFarUnit;
+    return exp2(-(double)b / kSmSteps) * ((double)n - (double)units / kEpsUnit);
+  }
+};
+
+FLINT_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+FLINT_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// the address of p (shared memory) in CTA r of the cluster
+template <typename T>
+FLINT_DEV T *cluster_at(T *p, int r) {
+  u64 out;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"(reinterpret_cast<u64>(p)), "r"(r));
+  return reinterpret_cast<T *>(out);
+}
+
+struct Sum {
+  uint32_t c;
+  double m;
 };
 
 struct Team {
   SampleShared *s;
   int rank, size, parity = 0;
-  FLINT_DEV void sync() { cg::this_cluster().sync(); }
+  FLINT_DEV void sync() {
+    cluster_arrive();
+    cluster_wait();
+  }
   template <typename T>
   FLINT_DEV T *of(T *p, int r) {
-    return cg::this_cluster().map_shared_rank(p, r);
+    return cluster_at(p, r);
   }
-  // every thread's (a, b) over the block: sums (kOp 0), or the largest a and b (kOp 1)
-  template <int kOp>
-  FLINT_DEV Sum2 block(unsigned long long a, double b) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  // The block's largest a, to every thread
+  FLINT_DEV u64 block_max(u64 a) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      const unsigned long long a2 = __shfl_xor_sync(0xffffffffu, a, o);
-      const double b2 = __shfl_xor_sync(0xffffffffu, b, o);
-      a = kOp ? (a > a2 ? a : a2) : a + a2;
-      b = kOp ? fmax(b, b2) : b + b2;
+      const u64 a2 = __shfl_xor_sync(0xffffffffu, a, o);
+      a = a > a2 ? a : a2;
     }
     __syncthreads();
-    if (lane == 0) s->red_a[w] = a, s->red_b[w] = b;
+    if ((threadIdx.x & 31) == 0) s->red_a[threadIdx.x >> 5] = a;
     __syncthreads();
-    a = s->red_a[0], b = s->red_b[0];
-    for (int i = 1; i < kSmWarps; ++i) {
-      a = kOp ? (a > s->red_a[i] ? a : s->red_a[i]) : a + s->red_a[i];
-      b = kOp ? fmax(b, s->red_b[i]) : b + s->red_b[i];
+    for (int i = 0; i < kSmWarps; ++i) a = a > s->red_a[i] ? a : s->red_a[i];
+    return a;
+  }
+  // Sums before each thread's (exclusive, in thread order); *total the block's
+  FLINT_DEV Sum scan(uint32_t c, double m, Sum *total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    uint32_t ic = c;
+    double im = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t c2 = __shfl_up_sync(0xffffffffu, ic, o);
+      const double m2 = __shfl_up_sync(0xffffffffu, im, o);
+      if (lane >= o) ic += c2, im += m2;
     }
-    return {a, b};
+    __syncthreads();
+    if (lane == 31) s->red_c[w] = ic, s->red_b[w] = im;
+    __syncthreads();
+    Sum before{0, 0.0}, all{0, 0.0};
+    for (int i = 0; i < kSmWarps; ++i) {
+      if (i == w) before = all;
+      all.c += s->red_c[i], all.m += s->red_b[i];
+    }
+    *total = all;
+    // lane 0's is the warps' sum exactly; the others' own value is taken out
+    // by the shuffle, not by a subtraction
+    const uint32_t pc = __shfl_up_sync(0xffffffffu, ic, 1);
+    const double pm = __shfl_up_sync(0xffffffffu, im, 1);
+    return lane ? Sum{before.c + pc, before.m + pm} : before;
   }
   // the CTAs' values to every CTA's slots; returns the set they are in
-  FLINT_DEV int exchange(Sum2 v) {
+  FLINT_DEV int exchange(u64 a, double b) {
     const int p = parity;
     parity ^= 1;
     if ((int)threadIdx.x < size) {
       auto *dst = of(&s->slot[p][rank], threadIdx.x);
-      dst->a = v.a, dst->b = v.b;
+      dst->a = a, dst->b = b;
     }
     sync();
     return p;
   }
-  template <int kOp>
-  FLINT_DEV Sum2 all(unsigned long long a, double b) {
-    const int p = exchange(block<kOp>(a, b));
-    a = s->slot[p][0].a, b = s->slot[p][0].b;
-    for (int r = 1; r < size; ++r) {
-      const unsigned long long a2 = s->slot[p][r].a;
-      const double b2 = s->slot[p][r].b;
-      a = kOp ? (a > a2 ? a : a2) : a + a2;
-      b = kOp ? fmax(b, b2) : b + b2;
-    }
-    return {a, b};
+  FLINT_DEV u64 all_max(u64 a) {
+    a = block_max(a);
+    const int p = exchange(a, 0.0);
+    for (int r = 0; r < size; ++r) a = a > s->slot[p][r].a ? a : s->slot[p][r].a;
+    return a;
   }
 };
 
@@ -163,130 +229,217 @@ struct Team {
 // of the order; otherwise the first whose running mass reaches `mass`.
 struct Goal {
   bool count;
-  unsigned long long want;
+  uint32_t want;
   double mass;
+  FLINT_DEV bool reached(uint32_t c, double m) const { return count ? c >= want : m >= mass; }
 };
 struct Cut {
-  unsigned long long key;  // the last kept element
-  double mass;             // mass down to it
+  u64 key;      // the last kept element
+  double mass;  // mass down to it
 };
+// Elements of the order between two keys, and what lies before them
+struct Range {
+  u64 lo, hi;
+  uint32_t n, above;
+  double mass_above;
+  FLINT_DEV int shift(int bits) const {
+    const int top = 64 - __clzll((long long)(hi - lo));
+    return top > bits ? top - bits : 0;
+  }
+  // to bin b of those that `shift` makes
+  FLINT_DEV void narrow(int b, int sh, uint32_t n_, uint32_t above_, double mass_) {
+    hi -= (u64)b << sh;
+    const u64 width = ((u64)1 << sh) - 1;
+    if (hi - lo > width) lo = hi - width;
+    n = n_, above = above_, mass_above = mass_;
+  }
+};
+
+// The bin in which a goal is reached, from the block's scan of kPer bins a
+// thread (before: the sums in front of the thread's bins); every thread gets
+// it with its sums, -1 if the bins do not reach the goal.
+template <int kPer>
+FLINT_DEV int pick(Team &t, const Goal &g, const uint32_t (&c)[kPer], const double (&m)[kPer],
+                   const Sum &before, uint32_t *n, uint32_t *above, double *mass) {
+  SampleShared &s = *t.s;
+  __syncthreads();
+  if (threadIdx.x == 0) s.found = 0x7fffffff;
+  __syncthreads();
+  int mine = 0x7fffffff;
+  Sum x = before, at = before;
+  uint32_t at_n = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const Sum y{x.c + c[i], x.m + m[i]};
+    if (mine == 0x7fffffff && c[i] && g.reached(y.c, y.m))
+      mine = kPer * (int)threadIdx.x + i, at = x, at_n = c[i];
+    x = y;
+  }
+  if (mine != 0x7fffffff) atomicMin(&s.found, mine);
+  __syncthreads();
+  const int b = s.found;
+  if (b == 0x7fffffff) return -1;
+  if (mine == b) s.at_n = at_n, s.at_above = at.c, s.at_mass = at.m;
+  __syncthreads();
+  *n = s.at_n, *above = s.at_above, *mass = s.at_mass;
+  return b;
+}
+
+// The cut among the m elements in this CTA's list, all of bin b (one CTA).
+FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, const Goal &goal) {
+  SampleShared &s = *t.s;
+  const int tid = threadIdx.x;
+  while (r.n > (uint32_t)kSmOrder) {
+    s.scnt[tid] = 0, s.seps[tid] = 0;
+    __syncthreads();
+    const int sh = r.shift(9);
+    for (int i = tid; i < m; i += kSmThreads) {
+      const u64 k = s.list[i];
+      if (k >= r.lo && k <= r.hi) {
+        const int x = (int)((r.hi - k) >> sh);
+        atomicAdd(&s.scnt[x], 1u);
+        atomicAdd(&s.seps[x], dist.units(key_z((uint32_t)(k >> 32)), b));
+      }
+    }
+    __syncthreads();
+    const uint32_t c[1] = {s.scnt[tid]};
+    const double ms[1] = {Dist::mass(c[0], s.seps[tid], b)};
+    Sum total;
+    Sum before = t.scan(c[0], ms[0], &total);
+    before.c += r.above, before.m += r.mass_above;
+    uint32_t n, above;
+    double mass;
+    int x = pick<1>(t, goal, c, ms, before, &n, &above, &mass);
+    if (x < 0) {
+      // the bins' masses round short of the goal: the last element
+      x = pick<1>(t, Goal{true, r.above + total.c, 0.0}, c, ms, before, &n, &above, &mass);
+    }
+    r.narrow(x, sh, n, above, mass);
+  }
+  // the last few, in order
+  if (tid == 0) s.mine_n = 0;
+  __syncthreads();
+  for (int i = tid; i < m; i += kSmThreads) {
+    const u64 k = s.list[i];
+    if (k >= r.lo && k <= r.hi) {
+      const uint32_t at = atomicAdd(&s.mine_n, 1u);
+      if (at < (uint32_t)kSmOrder) s.mine[at] = k;
+    }
+  }
+  __syncthreads();
+  const int n = min((int)s.mine_n, kSmOrder);
+  if (tid < n) {
+    const u64 k = s.mine[tid];
+    int before = 0;
+    for (int j = 0; j < n; ++j) before += s.mine[j] > k;
+    s.sorted[before] = k;
+  }
+  __syncthreads();
+  const u64 k = tid < n ? s.sorted[tid] : 0;
+  const uint32_t c[1] = {tid < n ? 1u : 0u};
+  const double p[1] = {tid < n ? (double)dist.p(key_z((uint32_t)(k >> 32))) : 0.0};
+  Sum total;
+  Sum before = t.scan(c[0], p[0], &total);
+  before.c += r.above, before.m += r.mass_above;
+  uint32_t x_n, x_above;
+  double x_mass;
+  int x = pick<1>(t, goal, c, p, before, &x_n, &x_above, &x_mass);
+  if (x < 0) x = pick<1>(t, Goal{true, r.above + total.c, 0.0}, c, p, before, &x_n, &x_above, &x_mass);
+  const u64 key = n ? s.sorted[x] : 0;
+  return {key, n ? x_mass + (double)dist.p(key_z((uint32_t)(key >> 32))) : r.mass_above};
+}
+
+// This CTA's bins summed over the cluster, to every CTA's tcnt and tmass.
+// bin_of(i): the level-0 bin whose units bin i holds.
+template <typename F>
+FLINT_DEV void merge_bins(Team &t, F bin_of) {
+  SampleShared &s = *t.s;
+  t.sync();  // every CTA's bins are complete
+  const int per = kSmBins / t.size;
+  for (int i = threadIdx.x; i < per; i += kSmThreads) {
+    const int b = t.rank * per + i;
+    uint32_t c = 0;
+    u64 e = 0;
+    for (int q = 0; q < t.size; ++q) c += t.of(s.cnt, q)[b], e += t.of(s.eps, q)[b];
+    const double mass = c ? Dist::mass(c, e, bin_of(b)) : 0.0;
+    for (int q = 0; q < t.size; ++q) t.of(s.tcnt, q)[b] = c, t.of(s.tmass, q)[b] = mass;
+  }
+  t.sync();
+}
 
 // The cut inside bin `b`, which holds n elements behind `above` earlier ones
 // with mass `mass_above`.  Every thread of the cluster takes part and gets
 // the same answer.
-FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, unsigned long long n,
-                      unsigned long long above, double mass_above, const Goal &goal) {
+FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32_t n,
+                      uint32_t above, double mass_above, const Goal &goal) {
   SampleShared &s = *t.s;
-  uint32_t klo = 0, khi = 0xffffffffu;
-  if (n > kSmList) {
-    uint32_t lo = 0xffffffffu, hi = 0;
-    for_elements(r, [&](float z, int) {
+  Range g{0, ~0ull, n, above, mass_above};
+  if (n > (uint32_t)kSmList) {
+    u64 lo = ~0ull, hi = 0;
+    for_elements(r, [&](float z, int i) {
       if (dist.bin(z) == b) {
-        const uint32_t k = zkey(z);
-        lo = min(lo, k), hi = max(hi, k);
+        const u64 k = order_key(z, i);
+        lo = k < lo ? k : lo, hi = k > hi ? k : hi;
       }
     });
-    // the largest of (hi, ~lo), both exact in a double
-    const Sum2 m = t.all<1>(hi, (double)(uint32_t)~lo);
-    khi = (uint32_t)m.a, klo = ~(uint32_t)m.b;
-    while (n > kSmList && klo < khi) {
-      const uint32_t mid = klo + (khi - klo) / 2;  // the upper half is (mid, khi]
-      unsigned long long cu = 0;
-      double mu = 0;
-      for_elements(r, [&](float z, int) {
-        const uint32_t k = zkey(z);
-        if (k > mid && k <= khi && dist.bin(z) == b) {
-          ++cu;
-          mu += (double)ex2(-dist(z));
+    g.hi = t.all_max(hi);
+    g.lo = ~t.all_max(~lo);
+    while (g.n > (uint32_t)kSmList) {
+      const int sh = g.shift(10);
+      for (int i = threadIdx.x; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
+      __syncthreads();
+      for_elements(r, [&](float z, int i) {
+        const u64 k = order_key(z, i);
+        if (k >= g.lo && k <= g.hi && dist.bin(z) == b) {
+          const int x = (int)((g.hi - k) >> sh);
+          atomicAdd(&s.cnt[x], 1u);
+          atomicAdd(&s.eps[x], dist.units(z, b));
         }
       });
-      const Sum2 u = t.all<0>(cu, mu);
-      if (u.a && (goal.count ? above + u.a >= goal.want : mass_above + u.b >= goal.mass)) {
-        klo = mid + 1;
-        n = u.a;
-      } else {
-        khi = mid;
-        n -= u.a, above += u.a, mass_above += u.b;
-      }
+      merge_bins(t, [&](int) { return b; });
+      const int i0 = 2 * threadIdx.x;
+      const uint32_t c[2] = {s.tcnt[i0], s.tcnt[i0 + 1]};
+      const double ms[2] = {s.tmass[i0], s.tmass[i0 + 1]};
+      Sum total;
+      Sum before = t.scan(c[0] + c[1], ms[0] + ms[1], &total);
+      before.c += g.above, before.m += g.mass_above;
+      uint32_t x_n, x_above;
+      double x_mass;
+      int x = pick<2>(t, goal, c, ms, before, &x_n, &x_above, &x_mass);
+      if (x < 0)
+        x = pick<2>(t, Goal{true, g.above + total.c, 0.0}, c, ms, before, &x_n, &x_above, &x_mass);
+      g.narrow(x, sh, x_n, x_above, x_mass);
     }
   }
-  if (n > kSmList) {
-    // one logit, more than kSmList times: cut by index
-    const float z0 = key_z(klo);
-    const double p = (double)ex2(-dist(z0));
-    double left = goal.count ? (double)(goal.want - above)
-                             : (p > 0 ? ceil((goal.mass - mass_above) / p) : (double)n);
-    left = fmin(fmax(left, 1.0), (double)n);
-    const unsigned long long keep = (unsigned long long)left;
-    unsigned long long mine = 0;
-    for_elements(r, [&](float z, int) { mine += z == z0; });
-    const Sum2 tot = t.block<0>(mine, 0);
-    const int q = t.exchange(tot);
-    unsigned long long before = 0;
-    for (int i = 0; i < t.rank; ++i) before += s.slot[q][i].a;
-    if (before < keep && before + tot.a >= keep) {
-      // this CTA has it: walk its elements in order, kSmThreads at a time
-      const float *z = reinterpret_cast<const float *>(r.z);
-      for (int base = 0; base < 4 * r.n4; base += kSmThreads) {
-        const int i = base + threadIdx.x;
-        const bool hit = i < 4 * r.n4 && z[i] == z0;
-        const int c = __syncthreads_count(hit);
-        if (before + c >= keep) {
-          const uint32_t m = __ballot_sync(0xffffffffu, hit);
-          const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-          if (lane == 0) s.red_a[w] = __popc(m);
-          __syncthreads();
-          unsigned long long at = before;
-          for (int k = 0; k < w; ++k) at += s.red_a[k];
-          if (hit && at + __popc(m & ((2u << lane) - 1u)) == keep) {
-            const unsigned long long key =
-                ((unsigned long long)klo << 32) | (0xffffffffu - (uint32_t)(r.index0 + i));
-            for (int k = 0; k < t.size; ++k) *t.of(&s.res_key, k) = key;
-          }
-          break;
-        }
-        before += c;
-      }
-    }
-    t.sync();
-    const Cut cut{s.res_key, mass_above + (double)keep * p};
-    t.sync();
-    return cut;
-  }
-  // gather into CTA 0 and order there
+  // gather into CTA 0, which has the rest to do
   if (t.rank == 0 && threadIdx.x == 0) s.list_n = 0;
   t.sync();
   uint32_t *ln = t.of(&s.list_n, 0);
-  unsigned long long *list = t.of(&s.list[0], 0);
+  u64 *list = t.of(&s.list[0], 0);
   for_elements(r, [&](float z, int i) {
-    const uint32_t k = zkey(z);
-    if (k >= klo && k <= khi && dist.bin(z) == b) {
+    const u64 k = order_key(z, i);
+    if (k >= g.lo && k <= g.hi && dist.bin(z) == b) {
       const uint32_t at = atomicAdd(ln, 1u);
-      if (at < (uint32_t)kSmList)
-        list[at] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)(r.index0 + i));
+      if (at < (uint32_t)kSmList) list[at] = k;
     }
   });
   t.sync();
   if (t.rank == 0) {
     const int m = min((int)s.list_n, kSmList);
-    for (int i = threadIdx.x; i < m; i += kSmThreads) {
-      const unsigned long long mine = s.list[i];
-      int before = 0;
-      for (int j = 0; j < m; ++j) before += s.list[j] > mine;
-      s.sorted[before] = mine;
-      s.lmass[before] = (double)ex2(-dist(key_z((uint32_t)(mine >> 32))));
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      double run = mass_above;
-      int i = 0;
-      for (; i < m; ++i) {
-        run += s.lmass[i];
-        if (goal.count ? above + i + 1 >= goal.want : run >= goal.mass) break;
+    if (n <= (uint32_t)kSmList && m > kSmOrder) {
+      u64 lo = ~0ull, hi = 0;
+      for (int i = threadIdx.x; i < m; i += kSmThreads) {
+        const u64 k = s.list[i];
+        lo = k < lo ? k : lo, hi = k > hi ? k : hi;
       }
-      if (i == m) --i;
-      const unsigned long long key = m ? s.sorted[i] : 0ull;
-      for (int k = 0; k < t.size; ++k) *t.of(&s.res_key, k) = key, *t.of(&s.res_mass, k) = run;
+      g.hi = t.block_max(hi);
+      g.lo = ~t.block_max(~lo);
+    }
+    g.n = m;
+    const Cut c = resolve_list(t, dist, b, m, g, goal);
+    if ((int)threadIdx.x < t.size) {
+      *t.of(&s.res_key, threadIdx.x) = c.key;
+      *t.of(&s.res_mass, threadIdx.x) = c.mass;
     }
   }
   t.sync();
@@ -295,16 +448,128 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, unsign
   return cut;
 }
 
-__global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ SampleArgs a) {
+struct Settings {
+  float T, top_p, min_p;
+  double u;
+};
+// the lowest logit that min-p keeps: p >= min_p is z >= M + T ln(min_p)
+FLINT_DEV float min_p_logit(float M, const Settings &p) {
+  return fminf(__double2float_ru((double)M + (double)p.T * log((double)p.min_p)), M);
+}
+FLINT_DEV void write_token(const SampleArgs &a, int row, int token, float z, float M, float T,
+                           double total) {
+  a.token[row] = token;
+  if (a.logprob) {
+    const double y = z == M ? 0.0 : ((double)z - (double)M) / (double)T;
+    a.logprob[row] = (float)(y - log(total));
+  }
+}
+
+// The rest of a short row, in the one CTA whose list holds its m candidates,
+// the first k of the order among them.
+FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k, bool greedy,
+                            const Settings &p) {
+  SampleShared &s = *t.s;
+  const int tid = threadIdx.x;
+  const float kInf = __int_as_float(0x7f800000);
+  if (m == 0) {
+    if (tid == 0) {
+      a.token[row] = -1;
+      if (a.logprob) a.logprob[row] = -kInf;
+    }
+    return;
+  }
+  u64 hi = 0, lo = ~0ull;
+  for (int i = tid; i < m; i += kSmThreads) {
+    const u64 x = s.list[i];
+    lo = x < lo ? x : lo, hi = x > hi ? x : hi;
+  }
+  hi = t.block_max(hi);
+  const float M = key_z((uint32_t)(hi >> 32));
+  if (greedy) {
+    if (tid == 0) {
+      a.token[row] = key_index(hi);
+      if (a.logprob) a.logprob[row] = 0.f;
+    }
+    return;
+  }
+  const Dist dist{M, __fdiv_rn(1.4426950408889634f, p.T)};
+  u64 from = 0;
+  if (m > kSmOrder) {
+    lo = ~t.block_max(~lo);
+    // (the masses are not looked at: any bin serves)
+    from = resolve_list(t, dist, 0, m, Range{lo, hi, (uint32_t)m, 0, 0.0},
+                        Goal{true, (uint32_t)min(k, m), 0.0}).key;
+    __syncthreads();
+  }
+  if (tid == 0) s.mine_n = 0;
+  __syncthreads();
+  for (int i = tid; i < m; i += kSmThreads) {
+    const u64 x = s.list[i];
+    if (x >= from) s.mine[atomicAdd(&s.mine_n, 1u)] = x;  // at most kSmOrder
+  }
+  __syncthreads();
+  const int n = (int)s.mine_n;
+  if (tid < n) {
+    const u64 x = s.mine[tid];
+    int before = 0;
+    for (int j = 0; j < n; ++j) before += s.mine[j] > x;
+    s.sorted[before] = x;
+  }
+  __syncthreads();
+  const int K = min(k, n);
+  u64 x = tid < K ? s.sorted[tid] : 0;
+  const float z = key_z((uint32_t)(x >> 32));
+  double w = tid < K ? (double)dist.p(z) : 0.0;
+  Sum total;
+  Sum before = t.scan(0, w, &total);
+  bool kept = w > 0;
+  if (p.top_p < 1.f) kept &= before.m < (double)p.top_p * total.m;
+  if (p.min_p > 0.f) kept &= z >= min_p_logit(M, p);
+  if (tid == 0) kept = true;  // the first one always
+  // in index order
+  if (tid == 0) s.mine_n = 0;
+  __syncthreads();
+  const u64 by_index = ((u64)(uint32_t)key_index(x) << 32) | (uint32_t)tid;
+  if (kept) s.mine[atomicAdd(&s.mine_n, 1u)] = by_index;
+  __syncthreads();
+  const int nk = (int)s.mine_n;
+  if (kept) {
+    int at = 0;
+    for (int j = 0; j < nk; ++j) at += s.mine[j] < by_index;
+    s.scnt[at] = (uint32_t)tid;  // place in the order
+  }
+  __syncthreads();
+  x = tid < nk ? s.sorted[s.scnt[tid]] : 0;
+  w = tid < nk ? (double)dist.p(key_z((uint32_t)(x >> 32))) : 0.0;
+  before = t.scan(0, w, &total);
+  const double goal = p.u * total.m;
+  // the first whose running mass passes the goal, or the last
+  if (tid == 0) s.found = nk - 1;
+  __syncthreads();
+  if (tid < nk && before.m + w > goal) atomicMin(&s.found, tid);
+  __syncthreads();
+  if (tid == s.found) write_token(a, row, key_index(x), key_z((uint32_t)(x >> 32)), M, p.T, total.m);
+}
+
+__global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) unsigned char smraw[];
   SampleShared &s = *reinterpret_cast<SampleShared *>(smraw);
   float *zs = reinterpret_cast<float *>(smraw + (sizeof(SampleShared) + 15) / 16 * 16);
-  cg::cluster_group cl = cg::this_cluster();
   Team t;
-  t.s = &s, t.rank = (int)cl.block_rank(), t.size = (int)cl.num_blocks();
+  t.s = &s;
+  {
+    uint32_t x;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(x));
+    t.rank = (int)x;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(x));
+    t.size = (int)x;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / t.size;
   const float kInf = __int_as_float(0x7f800000);
+  if (tid == 0) s.list_n = 0, s.mine_n = 0;
+  cluster_arrive();  // waited for before the first access to another CTA
 
   // this CTA's part of the row: [lo, hi), in whole 16-byte pieces of memory
   const int part = ((a.V + t.size - 1) / t.size + 3) & ~3;
@@ -315,9 +580,16 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
 
   pdl_wait();
   pdl_trigger();
+  const float T0 = a.temperature ? a.temperature[row] : 1.f;
+  const int k = a.top_k ? a.top_k[row] : 0;
+  Settings set;
+  set.T = T0 > 3.4e38f ? 3.4e38f : T0;
+  set.top_p = a.top_p ? a.top_p[row] : 1.f;
+  set.min_p = a.min_p ? a.min_p[row] : 0.f;
+  const float u0 = a.u[row];
   float top = -kInf;
   const float4 *src = reinterpret_cast<const float4 *>(a.logits + (g0 + lo - skip));
-#pragma unroll 4
+#pragma unroll 8
   for (int i = tid; i < r.n4; i += kSmThreads) {
     float4 v;
     const int e = r.index0 + 4 * i;
@@ -330,17 +602,76 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
       v.z = e + 2 >= lo && e + 2 < hi ? z[2] : -kInf;
       v.w = e + 3 >= lo && e + 3 < hi ? z[3] : -kInf;
     }
+    // NaN is never chosen: max(NaN, -inf) is -inf
+    v.x = fmaxf(v.x, -kInf), v.y = fmaxf(v.y, -kInf);
+    v.z = fmaxf(v.z, -kInf), v.w = fmaxf(v.w, -kInf);
     reinterpret_cast<float4 *>(zs)[i] = v;
-    top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));  // NaN drops out
+    top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
   }
-  for (int i = tid; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
-  const float T0 = a.temperature ? a.temperature[row] : 1.f;
-  const float T = T0 > 3.4e38f ? 3.4e38f : T0;
-  const int k = a.top_k ? a.top_k[row] : 0;
-  const float top_p = a.top_p ? a.top_p[row] : 1.f;
-  const float min_p = a.min_p ? a.min_p[row] : 0.f;
+  set.u = u0 > 0.f ? fmin((double)u0, 1.0) : 0.0;
+  const bool greedy = !(set.T > 0.f) || set.min_p > 1.f || k == 1 || set.top_p <= 0.f;
+  const int kk = greedy ? 1 : k;
 
-  const float M = key_z((uint32_t)t.all<1>(zkey(top), 0).a);
+  // ---- few kept tokens
+  if (kk > 0 && kk <= kSmShort) {
+    // the largest threshold found that at least kk threads' maxima reach
+    const uint32_t mine = zkey(top);
+    uint32_t a0 = __reduce_min_sync(0xffffffffu, mine), a1 = __reduce_max_sync(0xffffffffu, mine);
+    if (lane == 0) s.red_a[warp] = ((u64)a1 << 32) | a0;
+    __syncthreads();
+    for (int i = 0; i < kSmWarps; ++i) {
+      a0 = min(a0, (uint32_t)s.red_a[i]);
+      a1 = max(a1, (uint32_t)(s.red_a[i] >> 32));
+    }
+    // all reach a0; fewer than kk reach a1 + 1
+    uint32_t count = kSmThreads;
+    u64 end = (u64)a1 + 1;
+    while (end - a0 > 1 && count > (uint32_t)kk + kk / 4 + 2) {
+      const uint32_t mid = a0 + (uint32_t)((end - a0) / 2);
+      const uint32_t c = (uint32_t)__syncthreads_count(mine >= mid);
+      if (c >= (uint32_t)kk) a0 = mid, count = c;
+      else end = mid;
+    }
+    const uint32_t from = max(a0, kNoneKey + 1);
+    u64 *own = s.mine;  // and s.sorted: 2 kSmOrder entries
+    if (mine >= from) {
+      for (int i = tid; i < r.n4; i += kSmThreads) {
+        const float4 v = r.z[i];
+        const float z[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (zkey(z[j]) >= from) {
+            const uint32_t at = atomicAdd(&s.mine_n, 1u);
+            if (at < (uint32_t)kSmOrder) own[at] = order_key(z[j], r.index0 + 4 * i + j);
+          }
+      }
+    }
+    __syncthreads();
+    const uint32_t n = s.mine_n;
+    cluster_wait();
+    uint32_t *ln = t.of(&s.list_n, 0);
+    u64 *list = t.of(&s.list[0], 0);
+    // one that finds more than it can hold makes the total too large
+    if (tid == 0) s.at_n = atomicAdd(ln, n <= (uint32_t)kSmOrder ? n : (uint32_t)kSmList + 1);
+    __syncthreads();
+    const uint32_t base = s.at_n;
+    if (n <= (uint32_t)kSmOrder)
+      for (uint32_t i = tid; i < n; i += kSmThreads)
+        if (base + i < (uint32_t)kSmList) list[base + i] = own[i];
+    t.sync();
+    const uint32_t m = *ln;
+    cluster_arrive();  // CTA 0 stays until all have read it
+    if (m <= (uint32_t)kSmList) {
+      if (t.rank == 0) finish_short(t, a, row, (int)m, kk, greedy, set);
+      cluster_wait();
+      return;
+    }
+  }
+  cluster_wait();
+
+  // ---- the general row
+  for (int i = tid; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
+  const float M = key_z((uint32_t)t.all_max(zkey(top)));
   if (M == -kInf) {
     if (t.rank == 0 && tid == 0) {
       a.token[row] = -1;
@@ -349,207 +680,153 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
     t.sync();
     return;
   }
-  if (!(T > 0.f) || min_p > 1.f || k == 1 || top_p <= 0.f) {
-    // the first of the order: the lowest index of M
-    uint32_t best = 0xffffffffu;
+  if (greedy) {
+    // (all of a CTA's logits equal or nearly so) the lowest index of M
+    u64 best = 0;
     for_elements(r, [&](float z, int i) {
-      if (z == M) best = min(best, (uint32_t)(r.index0 + i));
+      if (z == M) best = max(best, order_key(z, i));
     });
-    const Sum2 m = t.all<1>((unsigned long long)(uint32_t)~best, 0);
+    best = t.all_max(best);
     if (t.rank == 0 && tid == 0) {
-      a.token[row] = (int)~(uint32_t)m.a;
+      a.token[row] = key_index(best);
       if (a.logprob) a.logprob[row] = 0.f;
     }
     t.sync();
     return;
   }
 
-  const Dist dist{M, __fdiv_rn(1.4426950408889634f, T)};
-  const bool use_k = k > 0 && k < a.V, use_p = top_p < 1.f;
-  unsigned long long cut = 0;  // kept: (z, index) at or before this in the order
+  const Dist dist{M, __fdiv_rn(1.4426950408889634f, set.T)};
+  const bool use_k = k > 0 && k < a.V, use_p = set.top_p < 1.f;
+  u64 cut = 0;  // kept: (z, index) at or before this in the order
   if (use_k || use_p) {
-    unsigned long long far_n = 0;
+    uint32_t far_n = 0;
     double far_mass = 0;
     for_elements(r, [&](float z, int) {
       const float d = dist(z);
       if (d < (float)kSmBins / kSmSteps) {
         const int b = (int)(d * kSmSteps);
-        const float e = 1.f - ex2((float)b * (1.f / kSmSteps) - d);
         atomicAdd(&s.cnt[b], 1u);
-        atomicAdd(&s.eps[b], (uint32_t)(fmaxf(e, 0.f) * kEpsUnit + 0.5f));
+        atomicAdd(&s.eps[b], dist.units(z, b));
       } else if (z > -kInf) {
         ++far_n;
         far_mass += (double)ex2(-d);
       }
     });
-    const Sum2 far = t.all<0>(far_n, far_mass);  // also: every CTA's bins are complete
-    {
-      const int per = kSmBins / t.size;
-      for (int i = tid; i < per; i += kSmThreads) {
-        const int b = t.rank * per + i;
-        unsigned long long c = 0, e = 0;
-        for (int q = 0; q < t.size; ++q) c += t.of(s.cnt, q)[b], e += t.of(s.eps, q)[b];
-        const double mass = exp2(-(double)b / kSmSteps) * ((double)c - (double)e / kEpsUnit);
-        for (int q = 0; q < t.size; ++q) t.of(s.tcnt, q)[b] = (uint32_t)c, t.of(s.tmass, q)[b] = mass;
-      }
-      t.sync();
-    }
-    // running count and mass before this thread's two bins (the same in every CTA)
-    unsigned long long c0 = s.tcnt[2 * tid], c1 = s.tcnt[2 * tid + 1], ex_c = c0 + c1;
-    double m0 = s.tmass[2 * tid], m1 = s.tmass[2 * tid + 1], ex_m = m0 + m1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long c2 = __shfl_up_sync(0xffffffffu, ex_c, o);
-      const double m2 = __shfl_up_sync(0xffffffffu, ex_m, o);
-      if (lane >= o) ex_c += c2, ex_m += m2;
-    }
-    __syncthreads();
-    if (lane == 31) s.red_a[warp] = ex_c, s.red_b[warp] = ex_m;
-    __syncthreads();
-    unsigned long long all_c = 0, pre_c = 0;
-    double all_m = 0, pre_m = 0;
-    for (int w = 0; w < kSmWarps; ++w) {
-      if (w == warp) pre_c = all_c, pre_m = all_m;
-      all_c += s.red_a[w], all_m += s.red_b[w];
-    }
-    ex_c = pre_c + ex_c - c0 - c1;
-    ex_m = pre_m + ex_m - (m0 + m1);
+    Sum far;
+    t.scan(far_n, far_mass, &far);
+    const int fp = t.exchange(far.c, far.m);
+    merge_bins(t, [](int b) { return b; });
+    far = {0, 0.0};
+    for (int i = 0; i < t.size; ++i) far.c += (uint32_t)s.slot[fp][i].a, far.m += s.slot[fp][i].b;
+    const uint32_t bc[2] = {s.tcnt[2 * tid], s.tcnt[2 * tid + 1]};
+    const double bm[2] = {s.tmass[2 * tid], s.tmass[2 * tid + 1]};
+    Sum all;
+    const Sum before = t.scan(bc[0] + bc[1], bm[0] + bm[1], &all);
 
     // the bin a goal falls in, and the cut in it
     auto search = [&](const Goal &g) {
-      __syncthreads();
-      if (tid == 0) s.found = kSmBins;
-      __syncthreads();
-      const bool in0 = c0 && (g.count ? ex_c + c0 >= g.want : ex_m + m0 >= g.mass);
-      const bool in1 = c1 && (g.count ? ex_c + c0 + c1 >= g.want : ex_m + m0 + m1 >= g.mass);
-      if (in0 || in1) atomicMin(&s.found, in0 ? 2 * tid : 2 * tid + 1);
-      __syncthreads();
-      const int b = s.found;
-      if (b < kSmBins) {
-        if (b / 2 == tid) {
-          s.red_a[0] = b & 1 ? c1 : c0;
-          s.red_a[1] = b & 1 ? ex_c + c0 : ex_c;
-          s.red_b[0] = b & 1 ? ex_m + m0 : ex_m;
-        }
-        __syncthreads();
-        const unsigned long long n = s.red_a[0], above = s.red_a[1];
-        const double mass = s.red_b[0];
-        __syncthreads();
-        return resolve(t, r, dist, b, n, above, mass, g);
-      }
-      if (!far.a) return Cut{0ull, all_m};  // nothing behind the bins: no cut
-      return resolve(t, r, dist, kSmBins, far.a, all_c, all_m, g);
+      uint32_t n, above;
+      double mass;
+      const int b = pick<2>(t, g, bc, bm, before, &n, &above, &mass);
+      if (b >= 0) return resolve(t, r, dist, b, n, above, mass, g);
+      if (!far.c) return Cut{0ull, all.m};  // nothing behind the bins: no cut
+      return resolve(t, r, dist, kSmBins, far.c, all.c, all.m, g);
     };
-    double mass = all_m + far.b;
-    if (use_k && (unsigned long long)k < all_c + far.a) {
-      const Cut c = search(Goal{true, (unsigned long long)k, 0.0});
+    double mass = all.m + far.m;
+    if (use_k && (uint32_t)k < all.c + far.c) {
+      const Cut c = search(Goal{true, (uint32_t)k, 0.0});
       cut = c.key;
       mass = c.mass;
     }
     if (use_p) {
-      const Cut c = search(Goal{false, 0, (double)top_p * mass});
+      const Cut c = search(Goal{false, 0, (double)set.top_p * mass});
       if (c.key > cut) cut = c.key;
     }
   }
-  if (min_p > 0.f) {
-    // p >= min_p: z at or above M + T ln(min_p)
-    const float zmin = __double2float_ru((double)M + (double)T * log((double)min_p));
-    const unsigned long long c = (unsigned long long)zkey(fminf(zmin, M)) << 32;
+  if (set.min_p > 0.f) {
+    const u64 c = (u64)zkey(min_p_logit(M, set)) << 32;
     if (c > cut) cut = c;
   }
 
-  // kept mass: a warp's elements are a contiguous piece of the CTA's
+  // kept mass: pieces of kSmChunk elements, one float4 a lane
   const float zc = cut ? key_z((uint32_t)(cut >> 32)) : -kInf;
-  const int ic = cut ? (int)(0xffffffffu - (uint32_t)cut) : 0x7fffffff;
+  const uint32_t ic = cut ? 0xffffffffu - (uint32_t)cut : 0x7fffffffu;
   auto p_of = [&](float z, int i) {
-    // index r.index0 + i <= ic among equals; -1 - ic wraps to "all" for a bare key
-    const bool kept = z > zc || (z == zc && (uint32_t)(r.index0 + i) <= (uint32_t)ic);
-    return kept ? ex2(-dist(z)) : 0.f;
+    // index at most ic among equals; a bare key's ic wraps to "all"
+    const bool kept = z > zc || (z == zc && (uint32_t)i <= ic);
+    return kept ? dist.p(z) : 0.f;
   };
-  const int per4 = (r.n4 + kSmWarps - 1) / kSmWarps;
-  const int w0 = min(r.n4, warp * per4), w1 = min(r.n4, w0 + per4);
-  double sum = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const float4 v = r.z[i];
-    sum += ((double)p_of(v.x, 4 * i) + p_of(v.y, 4 * i + 1)) +
-           ((double)p_of(v.z, 4 * i + 2) + p_of(v.w, 4 * i + 3));
-  }
+  const int chunks = (r.n4 + 31) / 32;  // at most kSmChunks
+  for (int c = warp; c < chunks; c += kSmWarps) {
+    const int i = 32 * c + lane, e = r.index0 + 4 * i;
+    float x = 0.f;
+    if (i < r.n4) {
+      const float4 v = r.z[i];
+      x = (p_of(v.x, e) + p_of(v.y, e + 1)) + (p_of(v.z, e + 2) + p_of(v.w, e + 3));
+    }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) s.chunk[c] = x;
+  }
   __syncthreads();
-  if (lane == 0) s.wsum[warp] = sum;
-  __syncthreads();
-  double mine = 0;
-  for (int w = 0; w < kSmWarps; ++w) mine += s.wsum[w];
-  const int q = t.exchange({0, mine});
-  double total = 0, u = a.u[row];
+  const double w = tid < chunks ? (double)s.chunk[tid] : 0.0;
+  Sum mine;
+  const Sum at = t.scan(0, w, &mine);
+  const int q = t.exchange(0, mine.m);
+  double total = 0;
   for (int i = 0; i < t.size; ++i) total += s.slot[q][i].b;
-  u = u > 0 ? fmin(u, 1.0) : 0.0;
-  const double goal = u * total;
-  // the CTA, then the warp, whose running mass passes the goal; the last one
+  const double goal = set.u * total;
+  // the CTA, then the piece, whose running mass passes the goal; the last one
   // with any mass if none does (u = 1, or the last bit of a sum)
   int cta = -1;
-  double run = 0, before = 0;
+  double run = 0, start = 0;
   for (int i = 0; i < t.size; ++i) {
     const double x = s.slot[q][i].b;
     if (x > 0) {
-      cta = i, before = run;
+      cta = i, start = run;
       if (run + x > goal) break;
     }
     run += x;
   }
   if (cta == t.rank) {
-    int w = 0;
-    double base = before;
-    run = before;
-    for (int i = 0; i < kSmWarps; ++i) {
-      if (s.wsum[i] > 0) {
-        w = i, base = run;
-        if (run + s.wsum[i] > goal) break;
-      }
-      run += s.wsum[i];
+    if (tid == 0) s.found = 0x7fffffff, s.mine_n = 0;
+    __syncthreads();
+    if (w > 0) {
+      atomicMax(&s.mine_n, (uint32_t)tid);  // the last piece with mass
+      if (start + at.m + w > goal) atomicMin(&s.found, tid);
     }
-    if (warp == w) {
-      int last = -1, hit = -1;  // row index
-      for (int i0 = w0; i0 < w1 && hit < 0; i0 += 32) {
-        const int i = i0 + lane;
-        float p[4] = {0.f, 0.f, 0.f, 0.f};
-        if (i < w1) {
-          const float4 v = r.z[i];
-          p[0] = p_of(v.x, 4 * i), p[1] = p_of(v.y, 4 * i + 1);
-          p[2] = p_of(v.z, 4 * i + 2), p[3] = p_of(v.w, 4 * i + 3);
-        }
-        const double own = ((double)p[0] + p[1]) + ((double)p[2] + p[3]);
-        double inc = own;
+    __syncthreads();
+    const int c = s.found == 0x7fffffff ? (int)s.mine_n : s.found;
+    if (tid == c) s.at_mass = start + at.m;
+    __syncthreads();
+    if (warp == 0) {
+      const int i = 32 * c + lane, e = r.index0 + 4 * i;
+      float p[4] = {0.f, 0.f, 0.f, 0.f};
+      if (i < r.n4) {
+        const float4 v = r.z[i];
+        p[0] = p_of(v.x, e), p[1] = p_of(v.y, e + 1), p[2] = p_of(v.z, e + 2), p[3] = p_of(v.w, e + 3);
+      }
+      const double own = ((double)p[0] + p[1]) + ((double)p[2] + p[3]);
+      double inc = own;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double x = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += x;
-        }
-        double at = base + (inc - own);
-        int mine_hit = -1, mine_last = -1;
-        for (int j = 0; j < 4; ++j) {
-          at += p[j];
-          if (p[j] > 0.f) {
-            mine_last = r.index0 + 4 * i + j;
-            if (mine_hit < 0 && at > goal) mine_hit = mine_last;
-          }
-        }
-        const uint32_t hits = __ballot_sync(0xffffffffu, mine_hit >= 0);
-        const uint32_t lasts = __ballot_sync(0xffffffffu, mine_last >= 0);
-        if (hits) hit = __shfl_sync(0xffffffffu, mine_hit, __ffs(hits) - 1);
-        if (lasts) last = __shfl_sync(0xffffffffu, mine_last, 31 - __clz(lasts));
-        base += __shfl_sync(0xffffffffu, inc, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
       }
-      if (hit < 0) hit = last;
-      if (lane == 0) {
-        a.token[row] = hit;
-        if (a.logprob) {
-          const float z = hit >= 0 ? zs[hit - r.index0] : M;
-          const double y = z == M ? 0.0 : ((double)z - (double)M) / (double)T;
-          a.logprob[row] = (float)(y - log(total));
+      double x = s.at_mass + (inc - own);
+      int hit = -1, last = -1;  // row indices
+      for (int j = 0; j < 4; ++j) {
+        x += p[j];
+        if (p[j] > 0.f) {
+          last = e + j;
+          if (hit < 0 && x > goal) hit = last;
         }
       }
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0);
+      const uint32_t lasts = __ballot_sync(0xffffffffu, last >= 0);
+      hit = hits ? __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1)
+                 : __shfl_sync(0xffffffffu, last, lasts ? 31 - __clz(lasts) : 0);
+      if (lane == 0) write_token(a, row, hit, hit >= 0 ? zs[hit - r.index0] : M, M, set.T, total);
     }
   }
   t.sync();  // no CTA leaves while another may still read its memory
