@@ -165,7 +165,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # current_stream().cuda_stream without the Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -321,16 +322,22 @@ def flint_int4_gemv_noalloc_status(stream=None) -> int:
 
 # ------------------------------------------------- the cache, its attention, sampling
 def _local(where: str, *tensors):
-    """Refuse tensors that are not on the current CUDA device: the call
-    launches there, and ``stream`` is one of its streams."""
-    import torch
-    dev = None
+    """The tensors' addresses.  Refuses tensors that are not on the current
+    CUDA device: the call launches there, and ``stream`` is one of its
+    streams."""
+    dev, ptrs = None, []
     for t in tensors:
-        if t is not None and not isinstance(t, int):
-            if dev is None:
-                dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-            if t.get_device() != dev or dev < 0:
+        if t is None or isinstance(t, int):
+            ptrs.append(t)
+            continue
+        on = t.get_device()
+        if on != dev:
+            import torch
+            if on < 0 or dev is not None or on != torch.cuda.current_device():
                 raise FlintError(FLINT_EINVAL, where)
+            dev = on
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
 def make_kv_cache(k, v, k_scale=None, v_scale=None) -> flint_kv_cache:
@@ -365,11 +372,11 @@ def flint_kv_append(cache: flint_kv_cache, q, q_stride: int, k, k_stride: int, v
                     theta: float, q_norm, k_norm, q_out, q_out_stride: int, ws, ws_bytes: int,
                     stream=None):
     """``cache``: from ``make_kv_cache``."""
-    _local("flint_kv_append", q, k, v, slots, pos, q_norm, k_norm, q_out, ws)
-    _check(lib().flint_kv_append(C.byref(cache), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
-                                 v_stride, T, q_heads, _ptr(slots), _ptr(pos), rope_dim,
-                                 1 if interleaved else 0, theta, _ptr(q_norm), _ptr(k_norm),
-                                 _ptr(q_out), q_out_stride, _ptr(ws), ws_bytes, _stream(stream)),
+    q, k, v, slots, pos, q_norm, k_norm, q_out, ws = _local(
+        "flint_kv_append", q, k, v, slots, pos, q_norm, k_norm, q_out, ws)
+    _check(lib().flint_kv_append(C.byref(cache), q, q_stride, k, k_stride, v, v_stride, T, q_heads,
+                                 slots, pos, rope_dim, 1 if interleaved else 0, theta, q_norm,
+                                 k_norm, q_out, q_out_stride, ws, ws_bytes, _stream(stream)),
            "flint_kv_append")
 
 
@@ -378,17 +385,17 @@ def flint_attn_decode(cache: flint_kv_cache, q, q_stride: int, B: int, q_heads: 
                       window: int, sinks, out, out_stride: int, lse, ws, ws_bytes: int,
                       stream=None):
     """``cache``: from ``make_kv_cache``."""
-    _local("flint_attn_decode", q, page_table, lens, prefix_pages, sinks, out, lse, ws)
-    _check(lib().flint_attn_decode(C.byref(cache), _ptr(q), q_stride, B, q_heads,
-                                   _ptr(page_table), max_pages, _ptr(lens), _ptr(prefix_pages),
-                                   prefix_len, scale, window, _ptr(sinks), _ptr(out), out_stride,
-                                   _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)),
+    q, page_table, lens, prefix_pages, sinks, out, lse, ws = _local(
+        "flint_attn_decode", q, page_table, lens, prefix_pages, sinks, out, lse, ws)
+    _check(lib().flint_attn_decode(C.byref(cache), q, q_stride, B, q_heads, page_table, max_pages,
+                                   lens, prefix_pages, prefix_len, scale, window, sinks, out,
+                                   out_stride, lse, ws, ws_bytes, _stream(stream)),
            "flint_attn_decode")
 
 
 def flint_sample(logits, stride: int, B: int, V: int, temperature, top_k, top_p, min_p, u, token,
                  logprob, stream=None):
-    _local("flint_sample", logits, temperature, top_k, top_p, min_p, u, token, logprob)
-    _check(lib().flint_sample(_ptr(logits), stride, B, V, _ptr(temperature), _ptr(top_k),
-                              _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(logprob),
-                              _stream(stream)), "flint_sample")
+    logits, temperature, top_k, top_p, min_p, u, token, logprob = _local(
+        "flint_sample", logits, temperature, top_k, top_p, min_p, u, token, logprob)
+    _check(lib().flint_sample(logits, stride, B, V, temperature, top_k, top_p, min_p, u, token,
+                              logprob, _stream(stream)), "flint_sample")

@@ -194,8 +194,13 @@ __global__ void __launch_bounds__(kApThreads)
 cudaError_t launch_append(const AppendArgs &a, double theta, cudaStream_t st) {
   AppendKArgs p;
   p.a = a;
-  for (int i = 0; i < 64; ++i)
-    p.freq[i] = 2 * i < a.rope_dim ? pow(theta, -2.0 * i / a.rope_dim) / 6.283185307179586476925 : 0.0;
+  // theta^(-2i / rope_dim) from its powers at the bits of i: seven calls of pow
+  // instead of 64 (2 us), six roundings instead of one
+  p.freq[0] = 1.0 / 6.283185307179586476925;
+  for (int bit = 1; 2 * bit < a.rope_dim; bit *= 2) {
+    const double f = pow(theta, -2.0 * bit / a.rope_dim);
+    for (int i = bit; i < 2 * bit && i < 64; ++i) p.freq[i] = p.freq[i - bit] * f;
+  }
   // Blocks of one token spread a short call over more SMs; blocks of four
   // share the angles' latency and keep more loads in flight.
   const bool many = a.T >= 4 * 148 * 4;

@@ -38,7 +38,7 @@ constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBins = 1024;       // steps of 1/32 in log2 units: d < 32
 constexpr float kSmSteps = 32.f;
 constexpr int kSmList = 2048;       // elements gathered in one CTA
-constexpr int kSmOrder = 512;       // elements put in order at once
+constexpr int kSmOrder = 128;       // elements put in order at once
 constexpr int kSmShort = 256;       // largest k of the short path
 constexpr int kSmMaxCluster = 8;
 constexpr int kSmChunk = 128;       // elements of a sum of the last step
@@ -58,7 +58,7 @@ struct SampleShared {
     };
     u64 list[kSmList];
   };
-  u64 sorted[kSmOrder], mine[kSmOrder];
+  u64 sorted[kSmShort], mine[kSmShort];
   uint32_t scnt[kSmThreads], seps[kSmThreads];
   // one exchange between the CTAs uses one of two sets of slots, in turn
   struct {
@@ -77,9 +77,10 @@ struct SampleShared {
   double at_mass;
 };
 
+// (below 2^-126: 0)
 FLINT_DEV float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -115,28 +116,44 @@ FLINT_DEV void for_elements(const RowPart &r, F f) {
 struct Dist {
   float M, c;
   // log2 of p(max) / p(z), >= 0; +inf where p = 0 (-inf)
-  FLINT_DEV float operator()(float z) const {
-    const float d = (M - z) * c;
-    return z == M ? 0.f : (d >= 0.f ? d : __int_as_float(0x7f800000));
-  }
+  FLINT_DEV float operator()(float z) const { return z == M ? 0.f : (M - z) * c; }
   FLINT_DEV float p(float z) const { return ex2(-(*this)(z)); }
-  FLINT_DEV int bin(float z) const {
-    const float d = (*this)(z);
-    return d < (float)kSmBins / kSmSteps ? (int)(d * kSmSteps)
-                                         : (z > -__int_as_float(0x7f800000) ? kSmBins : -1);
+  // The bin of d < 32: floor(32 d), found and turned back into a float
+  // (*edge) by adding 2^23 towards zero; conversions would queue for the unit
+  // that has the exponentials.
+  FLINT_DEV static int bin(float d, float *edge) {
+    const float t = __fmaf_rz(d, kSmSteps, 8388608.f);
+    *edge = t - 8388608.f;
+    return __float_as_int(t) & (kSmBins - 1);
   }
-  // what an element of bin b adds to the bin's integer, and the mass that a
-  // count and such a sum stand for: the shortfall from the bin's first value,
-  // or the value itself behind the bins
-  FLINT_DEV uint32_t units(float z, int b) const {
-    const float d = (*this)(z);
-    if (b == kSmBins) return (uint32_t)(ex2(-d) * kFarUnit + 0.5f);
-    const float e = 1.f - ex2((float)b * (1.f / kSmSteps) - d);
-    return (uint32_t)(fmaxf(e, 0.f) * kEpsUnit + 0.5f);
+  // What an element of a bin adds to the bin's integer: its shortfall
+  // e = 1 - 2^(edge/32 - d) from the bin's first value, by the series of the
+  // exponential (y < 0.0217: off by less than y^4/24 = 2^-26), or behind the
+  // bins its value itself.
+  FLINT_DEV static uint32_t units(float d, float edge) {
+    const float y = fmaxf(fmaf(edge, -1.f / kSmSteps, d), 0.f) * 0.69314718f;
+    const float e = y * fmaf(y, fmaf(y, 1.f / 6, -0.5f), 1.f);
+    return __float_as_uint(fmaf(e, kEpsUnit, 8388608.f)) & 0x7fffffu;
   }
+  FLINT_DEV static uint32_t far_units(float d) { return (uint32_t)(ex2(-d) * kFarUnit + 0.5f); }
+  FLINT_DEV uint32_t units_of(float z, int b) const {
+    const float d = (*this)(z);
+    return b == kSmBins ? far_units(d) : units(d, (float)b);
+  }
+  // the mass that a count and such a sum stand for
   FLINT_DEV static double mass(u64 n, u64 units, int b) {
     if (b == kSmBins) return (double)units / kFarUnit;
     return exp2(-(double)b / kSmSteps) * ((double)n - (double)units / kEpsUnit);
+  }
+};
+// The elements of bin b, by the distances it spans (b / 32 is exact)
+struct InBin {
+  float lo, hi;
+  bool far;
+  FLINT_DEV explicit InBin(int b)
+      : lo((float)b / kSmSteps), hi((float)(b + 1) / kSmSteps), far(b == kSmBins) {}
+  FLINT_DEV bool operator()(float d, float z) const {
+    return d >= lo && (far ? z > -__int_as_float(0x7f800000) : d < hi);
   }
 };
 
@@ -169,11 +186,10 @@ struct Team {
   }
   // The block's largest a, to every thread
   FLINT_DEV u64 block_max(u64 a) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const u64 a2 = __shfl_xor_sync(0xffffffffu, a, o);
-      a = a > a2 ? a : a2;
-    }
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(a >> 32));
+    const uint32_t lo =
+        __reduce_max_sync(0xffffffffu, (uint32_t)(a >> 32) == hi ? (uint32_t)a : 0u);
+    a = ((u64)hi << 32) | lo;
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s->red_a[threadIdx.x >> 5] = a;
     __syncthreads();
@@ -285,6 +301,27 @@ FLINT_DEV int pick(Team &t, const Goal &g, const uint32_t (&c)[kPer], const doub
   return b;
 }
 
+// An element for CTA 0's list.  The others keep theirs in their own list until
+// hand_over sends them together: a thread that adds to CTA 0's counter waits
+// for the answer through the cluster.  What does not fit is counted only.
+FLINT_DEV void collect(Team &t, u64 key) {
+  SampleShared &s = *t.s;
+  const uint32_t at = atomicAdd(t.rank ? &s.mine_n : &s.list_n, 1u);
+  if (at < (uint32_t)kSmList) s.list[at] = key;
+}
+FLINT_DEV void hand_over(Team &t) {
+  SampleShared &s = *t.s;
+  __syncthreads();
+  if (t.rank == 0) return;
+  const uint32_t n = s.mine_n;
+  if (threadIdx.x == 0) s.at_n = atomicAdd(t.of(&s.list_n, 0), n);
+  __syncthreads();
+  const uint32_t base = s.at_n;
+  u64 *list = t.of(&s.list[0], 0);
+  for (uint32_t i = threadIdx.x; i < n && base + i < (uint32_t)kSmList; i += kSmThreads)
+    list[base + i] = s.list[i];
+}
+
 // The cut among the m elements in this CTA's list, all of bin b (one CTA).
 FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, const Goal &goal) {
   SampleShared &s = *t.s;
@@ -298,7 +335,7 @@ FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, con
       if (k >= r.lo && k <= r.hi) {
         const int x = (int)((r.hi - k) >> sh);
         atomicAdd(&s.scnt[x], 1u);
-        atomicAdd(&s.seps[x], dist.units(key_z((uint32_t)(k >> 32)), b));
+        atomicAdd(&s.seps[x], dist.units_of(key_z((uint32_t)(k >> 32)), b));
       }
     }
     __syncthreads();
@@ -374,10 +411,11 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32
                       uint32_t above, double mass_above, const Goal &goal) {
   SampleShared &s = *t.s;
   Range g{0, ~0ull, n, above, mass_above};
+  const InBin in(b);
   if (n > (uint32_t)kSmList) {
     u64 lo = ~0ull, hi = 0;
     for_elements(r, [&](float z, int i) {
-      if (dist.bin(z) == b) {
+      if (in(dist(z), z)) {
         const u64 k = order_key(z, i);
         lo = k < lo ? k : lo, hi = k > hi ? k : hi;
       }
@@ -389,11 +427,12 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32
       for (int i = threadIdx.x; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
       __syncthreads();
       for_elements(r, [&](float z, int i) {
+        if (!in(dist(z), z)) return;
         const u64 k = order_key(z, i);
-        if (k >= g.lo && k <= g.hi && dist.bin(z) == b) {
+        if (k >= g.lo && k <= g.hi) {
           const int x = (int)((g.hi - k) >> sh);
           atomicAdd(&s.cnt[x], 1u);
-          atomicAdd(&s.eps[x], dist.units(z, b));
+          atomicAdd(&s.eps[x], dist.units_of(z, b));
         }
       });
       merge_bins(t, [&](int) { return b; });
@@ -412,17 +451,15 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32
     }
   }
   // gather into CTA 0, which has the rest to do
-  if (t.rank == 0 && threadIdx.x == 0) s.list_n = 0;
+  if (threadIdx.x == 0) s.mine_n = 0, s.list_n = 0;
   t.sync();
-  uint32_t *ln = t.of(&s.list_n, 0);
-  u64 *list = t.of(&s.list[0], 0);
   for_elements(r, [&](float z, int i) {
-    const u64 k = order_key(z, i);
-    if (k >= g.lo && k <= g.hi && dist.bin(z) == b) {
-      const uint32_t at = atomicAdd(ln, 1u);
-      if (at < (uint32_t)kSmList) list[at] = k;
+    if (in(dist(z), z)) {
+      const u64 k = order_key(z, i);
+      if (k >= g.lo && k <= g.hi) collect(t, k);
     }
   });
+  hand_over(t);
   t.sync();
   if (t.rank == 0) {
     const int m = min((int)s.list_n, kSmList);
@@ -495,7 +532,7 @@ FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k,
   }
   const Dist dist{M, __fdiv_rn(1.4426950408889634f, p.T)};
   u64 from = 0;
-  if (m > kSmOrder) {
+  if (m > kSmShort) {
     lo = ~t.block_max(~lo);
     // (the masses are not looked at: any bin serves)
     from = resolve_list(t, dist, 0, m, Range{lo, hi, (uint32_t)m, 0, 0.0},
@@ -506,7 +543,7 @@ FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k,
   __syncthreads();
   for (int i = tid; i < m; i += kSmThreads) {
     const u64 x = s.list[i];
-    if (x >= from) s.mine[atomicAdd(&s.mine_n, 1u)] = x;  // at most kSmOrder
+    if (x >= from) s.mine[atomicAdd(&s.mine_n, 1u)] = x;  // at most kSmShort
   }
   __syncthreads();
   const int n = (int)s.mine_n;
@@ -633,33 +670,19 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
       else end = mid;
     }
     const uint32_t from = max(a0, kNoneKey + 1);
-    u64 *own = s.mine;  // and s.sorted: 2 kSmOrder entries
     if (mine >= from) {
       for (int i = tid; i < r.n4; i += kSmThreads) {
         const float4 v = r.z[i];
         const float z[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (zkey(z[j]) >= from) {
-            const uint32_t at = atomicAdd(&s.mine_n, 1u);
-            if (at < (uint32_t)kSmOrder) own[at] = order_key(z[j], r.index0 + 4 * i + j);
-          }
+          if (zkey(z[j]) >= from) collect(t, order_key(z[j], r.index0 + 4 * i + j));
       }
     }
-    __syncthreads();
-    const uint32_t n = s.mine_n;
     cluster_wait();
-    uint32_t *ln = t.of(&s.list_n, 0);
-    u64 *list = t.of(&s.list[0], 0);
-    // one that finds more than it can hold makes the total too large
-    if (tid == 0) s.at_n = atomicAdd(ln, n <= (uint32_t)kSmOrder ? n : (uint32_t)kSmList + 1);
-    __syncthreads();
-    const uint32_t base = s.at_n;
-    if (n <= (uint32_t)kSmOrder)
-      for (uint32_t i = tid; i < n; i += kSmThreads)
-        if (base + i < (uint32_t)kSmList) list[base + i] = own[i];
+    hand_over(t);
     t.sync();
-    const uint32_t m = *ln;
+    const uint32_t m = *t.of(&s.list_n, 0);
     cluster_arrive();  // CTA 0 stays until all have read it
     if (m <= (uint32_t)kSmList) {
       if (t.rank == 0) finish_short(t, a, row, (int)m, kk, greedy, set);
@@ -704,9 +727,10 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
     for_elements(r, [&](float z, int) {
       const float d = dist(z);
       if (d < (float)kSmBins / kSmSteps) {
-        const int b = (int)(d * kSmSteps);
+        float edge;
+        const int b = Dist::bin(d, &edge);
         atomicAdd(&s.cnt[b], 1u);
-        atomicAdd(&s.eps[b], dist.units(z, b));
+        atomicAdd(&s.eps[b], Dist::units(d, edge));
       } else if (z > -kInf) {
         ++far_n;
         far_mass += (double)ex2(-d);
