@@ -768,11 +768,6 @@ namespace {
 template <typename... KArgs, typename... Args>
 cudaError_t at_launch(void (*kernel)(KArgs...), int grid, int block, size_t smem, cudaStream_t st,
                       Args... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
@@ -793,6 +788,8 @@ cudaError_t launch_parts(const CUtensorMap &k, const CUtensorMap &v, const AttnK
   const size_t smem = 1024 + (size_t)Tile::kStages * 2 * Tile::kBytes +
                       sizeof(float) * AtJoin<kD, kNT>::kFloats + sizeof(float2) * kAtWarps * 8 * kNT +
                       (kPre ? 0 : sizeof(int32_t) * ((size_t)a.B + 1));
+  const cudaError_t e = smem_once<k_attn_parts<kD, kF8, kNT, kPre>>(a.dev, 200 * 1024);
+  if (e != cudaSuccess) return e;
   return at_launch(k_attn_parts<kD, kF8, kNT, kPre>, grid, kAtThreads, smem, st, k, v, a);
 }
 
@@ -874,6 +871,7 @@ cudaError_t launch_attn(const AttnArgs &p, char *ws, cudaStream_t st) {
     return e;
   const AttnLayout L = attn_layout(p.B, p.q_heads, p.c.heads, p.c.head_dim);
   AttnK a{};
+  a.dev = dev;
   a.q = p.q, a.q_stride = p.q_stride, a.B = p.B, a.H = p.c.heads, a.G = p.q_heads / p.c.heads;
   a.table = p.page_table, a.max_pages = p.max_pages, a.lens = p.lens;
   a.prefix_pages = p.prefix_pages, a.prefix_len = p.prefix_len, a.window = p.window;

@@ -36,6 +36,7 @@ struct AttnK {
   float2 *ml_own, *ml_pre;
   int ctas_pre;              // CTAs of the prefix list
   int pre_rows, pre_keys;    // rows of a prefix unit, keys of its tiles
+  int dev;
   int behind_prefix;         // the own keys' kernel follows a prefix kernel
 };
 

@@ -545,8 +545,7 @@ template <int kD, bool kF8>
 cudaError_t launch_as(const CUtensorMap &k, const CUtensorMap &v, const AttnK &a, int box_rows,
                       cudaStream_t st) {
   using C = PreCfg<kD, kF8>;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_prefix<kD, kF8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  const cudaError_t e = smem_once<k_attn_prefix<kD, kF8>>(a.dev, C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas_pre);

@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/flint.h"
 
 namespace flint {
@@ -234,5 +236,17 @@ struct AttnArgs {
 };
 size_t attn_ws_bytes(int B, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attn(const AttnArgs &a, char *ws, cudaStream_t st);
+
+// Lets kKernel have `bytes` of dynamic shared memory, once a device: the call
+// costs 1.7 us of host time.
+template <auto kKernel>
+cudaError_t smem_once(int dev, size_t bytes) {
+  static std::atomic<uint64_t> done{0};  // one bit per device
+  if (dev < 64 && ((done.load(std::memory_order_relaxed) >> dev) & 1u)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace flint

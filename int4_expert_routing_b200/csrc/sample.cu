@@ -862,8 +862,9 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st) {
   const int part = ((a.V + size - 1) / size + 3) & ~3;
   const size_t smem = (sizeof(SampleShared) + 15) / 16 * 16 + (size_t)(part + 4) * 4;
   note_step("sample attribute");
-  cudaError_t e = cudaFuncSetAttribute(k_sample, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       200 * 1024);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = smem_once<k_sample>(dev, 200 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.B * size);
