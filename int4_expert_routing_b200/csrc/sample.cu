@@ -3,9 +3,10 @@
 //
 // No sort of the vocabulary: the kept set is "everything from a cut on" in
 // the order (logit down, index up), so only the cut is searched.  A cluster
-// of CTAs takes a row and holds it in shared memory, read from HBM once.  An
-// element's place in the order is one 64-bit key (logit, then index), so that
-// equal logits need no case of their own.
+// of CTAs takes a row; each holds its part in shared memory, read from HBM
+// once, or where the batch fills the GPU with smaller clusters reads it again
+// from L2.  An element's place in the order is one 64-bit key (logit, then
+// index), so that equal logits need no case of their own.
 //
 // Few kept tokens (top-k of up to kSmShort, greedy rows): each CTA finds a
 // threshold that at least k of its threads' largest logits reach, and hands
@@ -16,18 +17,19 @@
 //   1. the largest logit M;
 //   2. a histogram over d = (M - z) log2(e) / temperature in steps of 1/32:
 //      each bin's count and mass.  The mass is summed in integers: within a
-//      bin 2^-d is 2^(-bin/32) (1 - e) with e < 0.0215, and the sum of e in
-//      units of 2^-22 fits 32 bits for the 2^15 elements of a CTA and does not
-//      depend on the order of the atomics;
+//      bin 2^-d is 2^(-bin/32) (1 - e) with e < 0.0217, and the sum of e in
+//      units of 2^-19 fits 32 bits for all of a row;
 //   3. the bins' running count and mass name the bin a cut falls in.  Its
 //      elements are gathered into one CTA, which narrows them down by 512 bins
 //      of the key and orders the last few.  More than fit there (flat rows,
 //      equal logits) are narrowed down by bins of the key in the cluster first;
-//   4. the kept mass in index order (pieces of 128 elements in fp32, their sums
-//      in fp64, fixed order), and the token whose running mass passes u times
-//      the total.
-// Every sum has a fixed order or is an integer, so a row's result does not
-// vary between runs, nor with the other rows.
+//   4. the kept mass in index order, p in units of 2^-44, by pieces of 128
+//      elements, and the token whose running mass passes u times the total.
+// Sums over many elements are integers, and the few in floating point go over
+// the order or the bins: a row's result is the same for every run, batch,
+// cluster size and alignment.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -42,9 +44,10 @@ constexpr int kSmOrder = 128;       // elements put in order at once
 constexpr int kSmShort = 256;       // largest k of the short path
 constexpr int kSmMaxCluster = 8;
 constexpr int kSmChunk = 128;       // elements of a sum of the last step
-constexpr int kSmChunks = FLINT_MAX_VOCAB / kSmMaxCluster / kSmChunk + 2;
-constexpr float kEpsUnit = 4194304.f;          // 2^22
-constexpr float kFarUnit = 281474976710656.f;  // 2^48
+constexpr int kSmChunks = FLINT_MAX_VOCAB / kSmChunk + 2;
+constexpr int kSmHold = 160 * 1024;  // bytes of a row that a CTA holds at most
+constexpr float kEpsUnit = 524288.f;          // 2^19
+constexpr float kFarUnit = 35184372088832.f;  // 2^45: 2^13 for the first behind the bins
 constexpr uint32_t kNoneKey = 0x007fffffu;     // -inf: never chosen
 
 typedef unsigned long long u64;
@@ -56,25 +59,25 @@ struct SampleShared {
       uint32_t tcnt[kSmBins];               // the cluster's
       double tmass[kSmBins];
     };
-    u64 list[kSmList];
+    long long chunk[kSmChunks];  // the last step's
   };
+  u64 list[kSmList];
   u64 sorted[kSmShort], mine[kSmShort];
   uint32_t scnt[kSmThreads], seps[kSmThreads];
   // one exchange between the CTAs uses one of two sets of slots, in turn
   struct {
-    u64 a;
-    double b;
+    u64 a, b;
   } slot[2][kSmMaxCluster];
   uint32_t red_c[kSmWarps];
   u64 red_a[kSmWarps];
   double red_b[kSmWarps];
-  float chunk[kSmChunks];
-  u64 res_key;
-  double res_mass;
+  u64 res_key[2];
+  double res_mass[2];
   uint32_t list_n, mine_n;
   int found;
   uint32_t at_n, at_above;
   double at_mass;
+  long long at_sum;
 };
 
 // (below 2^-126: 0)
@@ -94,24 +97,51 @@ FLINT_DEV u64 order_key(float z, int index) {
 }
 FLINT_DEV int key_index(u64 k) { return (int)(0xffffffffu - (uint32_t)k); }
 
-// A row's view in one CTA: z[0 .. 4 n4) with index0 the row index of z[0]
-// (it may start up to 3 elements early; those hold -inf, as NaN ones do).
+// A row's view in one CTA: 4 n4 elements from row index index0 on, of which
+// [lo, hi) are the CTA's (the pieces are 16 bytes of memory, so the first may
+// start up to 3 elements early and the last end late; those read as -inf).
+// kHeld: in shared memory, where NaN reads as -inf too.
+template <bool kHeld>
 struct RowPart {
   const float4 *z;
   int n4;
-  int index0;
-};
-
-template <typename F>
-FLINT_DEV void for_elements(const RowPart &r, F f) {
-  for (int i = threadIdx.x; i < r.n4; i += kSmThreads) {
-    const float4 v = r.z[i];
-    f(v.x, r.index0 + 4 * i);
-    f(v.y, r.index0 + 4 * i + 1);
-    f(v.z, r.index0 + 4 * i + 2);
-    f(v.w, r.index0 + 4 * i + 3);
+  int index0, lo, hi;
+  FLINT_DEV float4 load(int i) const {
+    if (kHeld) return z[i];
+    const int e = index0 + 4 * i;
+    if (e >= lo && e + 4 <= hi) return __ldcg(z + i);
+    const float *p = reinterpret_cast<const float *>(z + i);
+    const float kNone = -__int_as_float(0x7f800000);
+    float4 v;
+    v.x = e >= lo && e < hi ? p[0] : kNone;
+    v.y = e + 1 >= lo && e + 1 < hi ? p[1] : kNone;
+    v.z = e + 2 >= lo && e + 2 < hi ? p[2] : kNone;
+    v.w = e + 3 >= lo && e + 3 < hi ? p[3] : kNone;
+    return v;
   }
-}
+  static constexpr int kAhead = kHeld ? 2 : 8;
+  // f(logit, row index) for this thread's elements
+  template <typename F>
+  FLINT_DEV void each(F f) const {
+    const float kNone = -__int_as_float(0x7f800000);
+    for (int i0 = threadIdx.x; i0 < n4; i0 += kAhead * kSmThreads) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kSmThreads;
+        v[u] = i < n4 ? load(i) : make_float4(kNone, kNone, kNone, kNone);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int e = index0 + 4 * (i0 + u * kSmThreads);
+        f(v[u].x, e);
+        f(v[u].y, e + 1);
+        f(v[u].z, e + 2);
+        f(v[u].w, e + 3);
+      }
+    }
+  }
+};
 
 struct Dist {
   float M, c;
@@ -136,6 +166,18 @@ struct Dist {
     return __float_as_uint(fmaf(e, kEpsUnit, 8388608.f)) & 0x7fffffu;
   }
   FLINT_DEV static uint32_t far_units(float d) { return (uint32_t)(ex2(-d) * kFarUnit + 0.5f); }
+  // p <= 1 in units of 2^-44, as hi 2^22 + lo, added to the sums of both: hi
+  // is p to the nearest 2^-22 (adding 2^23 leaves it in the low bits), lo what
+  // that rounded off.  The constants in the bits go out at the end (whole).
+  FLINT_DEV static void add_units(float p, uint32_t &hi, uint32_t &lo) {
+    const float t = fmaf(p, 4194304.f, 8388608.f);
+    const float r = fmaf(t - 8388608.f, -1.f / 4194304.f, p);
+    hi += __float_as_uint(t);
+    lo += __float_as_uint(fmaf(r, 17592186044416.f, 12582912.f));
+  }
+  FLINT_DEV static long long whole(uint32_t hi, uint32_t lo, uint32_t n) {
+    return ((long long)(hi - n * 0x4B000000u) << 22) + (int)(lo - n * 0x4B400000u);
+  }
   FLINT_DEV uint32_t units_of(float z, int b) const {
     const float d = (*this)(z);
     return b == kSmBins ? far_units(d) : units(d, (float)b);
@@ -175,7 +217,7 @@ struct Sum {
 
 struct Team {
   SampleShared *s;
-  int rank, size, parity = 0;
+  int rank, size, parity = 0, resolved = 0;
   FLINT_DEV void sync() {
     cluster_arrive();
     cluster_wait();
@@ -195,6 +237,26 @@ struct Team {
     __syncthreads();
     for (int i = 0; i < kSmWarps; ++i) a = a > s->red_a[i] ? a : s->red_a[i];
     return a;
+  }
+  // Sums before each thread's, of integers that fit 63 bits
+  FLINT_DEV long long scan(long long x, long long *total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) s->red_a[w] = (u64)inc;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int i = 0; i < kSmWarps; ++i) {
+      if (i == w) before = all;
+      all += (long long)s->red_a[i];
+    }
+    *total = all;
+    return before + inc - x;
   }
   // Sums before each thread's (exclusive, in thread order); *total the block's
   FLINT_DEV Sum scan(uint32_t c, double m, Sum *total) {
@@ -222,20 +284,21 @@ struct Team {
     const double pm = __shfl_up_sync(0xffffffffu, im, 1);
     return lane ? Sum{before.c + pc, before.m + pm} : before;
   }
-  // the CTAs' values to every CTA's slots; returns the set they are in
-  FLINT_DEV int exchange(u64 a, double b) {
+  // the CTAs' values to every CTA's slots, there after the next sync; returns
+  // the set they are in
+  FLINT_DEV int post(u64 a, u64 b) {
     const int p = parity;
     parity ^= 1;
     if ((int)threadIdx.x < size) {
       auto *dst = of(&s->slot[p][rank], threadIdx.x);
       dst->a = a, dst->b = b;
     }
-    sync();
     return p;
   }
   FLINT_DEV u64 all_max(u64 a) {
     a = block_max(a);
-    const int p = exchange(a, 0.0);
+    const int p = post(a, 0);
+    sync();
     for (int r = 0; r < size; ++r) a = a > s->slot[p][r].a ? a : s->slot[p][r].a;
     return a;
   }
@@ -320,6 +383,7 @@ FLINT_DEV void hand_over(Team &t) {
   u64 *list = t.of(&s.list[0], 0);
   for (uint32_t i = threadIdx.x; i < n && base + i < (uint32_t)kSmList; i += kSmThreads)
     list[base + i] = s.list[i];
+  if (threadIdx.x == 0) s.mine_n = 0;
 }
 
 // The cut among the m elements in this CTA's list, all of bin b (one CTA).
@@ -397,9 +461,13 @@ FLINT_DEV void merge_bins(Team &t, F bin_of) {
     const int b = t.rank * per + i;
     uint32_t c = 0;
     u64 e = 0;
-    for (int q = 0; q < t.size; ++q) c += t.of(s.cnt, q)[b], e += t.of(s.eps, q)[b];
+#pragma unroll
+    for (int q = 0; q < kSmMaxCluster; ++q)
+      if (q < t.size) c += t.of(s.cnt, q)[b], e += t.of(s.eps, q)[b];
     const double mass = c ? Dist::mass(c, e, bin_of(b)) : 0.0;
-    for (int q = 0; q < t.size; ++q) t.of(s.tcnt, q)[b] = c, t.of(s.tmass, q)[b] = mass;
+#pragma unroll
+    for (int q = 0; q < kSmMaxCluster; ++q)
+      if (q < t.size) t.of(s.tcnt, q)[b] = c, t.of(s.tmass, q)[b] = mass;
   }
   t.sync();
 }
@@ -407,14 +475,15 @@ FLINT_DEV void merge_bins(Team &t, F bin_of) {
 // The cut inside bin `b`, which holds n elements behind `above` earlier ones
 // with mass `mass_above`.  Every thread of the cluster takes part and gets
 // the same answer.
-FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32_t n,
+template <bool kHeld>
+FLINT_DEV Cut resolve(Team &t, const RowPart<kHeld> &r, const Dist &dist, int b, uint32_t n,
                       uint32_t above, double mass_above, const Goal &goal) {
   SampleShared &s = *t.s;
   Range g{0, ~0ull, n, above, mass_above};
   const InBin in(b);
   if (n > (uint32_t)kSmList) {
     u64 lo = ~0ull, hi = 0;
-    for_elements(r, [&](float z, int i) {
+    r.each([&](float z, int i) {
       if (in(dist(z), z)) {
         const u64 k = order_key(z, i);
         lo = k < lo ? k : lo, hi = k > hi ? k : hi;
@@ -426,7 +495,7 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32
       const int sh = g.shift(10);
       for (int i = threadIdx.x; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
       __syncthreads();
-      for_elements(r, [&](float z, int i) {
+      r.each([&](float z, int i) {
         if (!in(dist(z), z)) return;
         const u64 k = order_key(z, i);
         if (k >= g.lo && k <= g.hi) {
@@ -451,9 +520,7 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32
     }
   }
   // gather into CTA 0, which has the rest to do
-  if (threadIdx.x == 0) s.mine_n = 0, s.list_n = 0;
-  t.sync();
-  for_elements(r, [&](float z, int i) {
+  r.each([&](float z, int i) {
     if (in(dist(z), z)) {
       const u64 k = order_key(z, i);
       if (k >= g.lo && k <= g.hi) collect(t, k);
@@ -461,6 +528,8 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32
   });
   hand_over(t);
   t.sync();
+  const int at = t.resolved & 1;  // (a slow CTA may still read the other)
+  ++t.resolved;
   if (t.rank == 0) {
     const int m = min((int)s.list_n, kSmList);
     if (n <= (uint32_t)kSmList && m > kSmOrder) {
@@ -474,15 +543,14 @@ FLINT_DEV Cut resolve(Team &t, const RowPart &r, const Dist &dist, int b, uint32
     }
     g.n = m;
     const Cut c = resolve_list(t, dist, b, m, g, goal);
+    if (threadIdx.x == 0) s.list_n = 0;
     if ((int)threadIdx.x < t.size) {
-      *t.of(&s.res_key, threadIdx.x) = c.key;
-      *t.of(&s.res_mass, threadIdx.x) = c.mass;
+      *t.of(&s.res_key[at], threadIdx.x) = c.key;
+      *t.of(&s.res_mass[at], threadIdx.x) = c.mass;
     }
   }
   t.sync();
-  const Cut cut{s.res_key, s.res_mass};
-  t.sync();
-  return cut;
+  return {s.res_key[at], s.res_mass[at]};
 }
 
 struct Settings {
@@ -494,11 +562,11 @@ FLINT_DEV float min_p_logit(float M, const Settings &p) {
   return fminf(__double2float_ru((double)M + (double)p.T * log((double)p.min_p)), M);
 }
 FLINT_DEV void write_token(const SampleArgs &a, int row, int token, float z, float M, float T,
-                           double total) {
+                           long long total) {
   a.token[row] = token;
   if (a.logprob) {
     const double y = z == M ? 0.0 : ((double)z - (double)M) / (double)T;
-    a.logprob[row] = (float)(y - log(total));
+    a.logprob[row] = (float)(y - log((double)total * (1.0 / 17592186044416.0)));
   }
 }
 
@@ -578,21 +646,27 @@ FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k,
   }
   __syncthreads();
   x = tid < nk ? s.sorted[s.scnt[tid]] : 0;
-  w = tid < nk ? (double)dist.p(key_z((uint32_t)(x >> 32))) : 0.0;
-  before = t.scan(0, w, &total);
-  const double goal = p.u * total.m;
-  // the first whose running mass passes the goal, or the last
+  long long units = 0, sum;
+  if (tid < nk) {
+    uint32_t uh = 0, ul = 0;
+    Dist::add_units(dist.p(key_z((uint32_t)(x >> 32))), uh, ul);
+    units = Dist::whole(uh, ul, 1);
+  }
+  const long long at = t.scan(units, &sum);
+  const double goal = p.u * (double)sum;
+  // the first whose running mass passes the goal, or the last (u = 1)
   if (tid == 0) s.found = nk - 1;
   __syncthreads();
-  if (tid < nk && before.m + w > goal) atomicMin(&s.found, tid);
+  if (tid < nk && (double)(at + units) > goal) atomicMin(&s.found, tid);
   __syncthreads();
-  if (tid == s.found) write_token(a, row, key_index(x), key_z((uint32_t)(x >> 32)), M, p.T, total.m);
+  if (tid == s.found) write_token(a, row, key_index(x), key_z((uint32_t)(x >> 32)), M, p.T, sum);
 }
 
-__global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
+template <bool kHeld>
+__global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) unsigned char smraw[];
   SampleShared &s = *reinterpret_cast<SampleShared *>(smraw);
-  float *zs = reinterpret_cast<float *>(smraw + (sizeof(SampleShared) + 15) / 16 * 16);
+  float4 *held = reinterpret_cast<float4 *>(smraw + (sizeof(SampleShared) + 15) / 16 * 16);
   Team t;
   t.s = &s;
   {
@@ -613,7 +687,9 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
   const int lo = min(a.V, t.rank * part), hi = min(a.V, lo + part);
   const int64_t g0 = (int64_t)row * a.stride;
   const int skip = (int)((g0 + lo) & 3);
-  RowPart r{reinterpret_cast<const float4 *>(zs), (skip + hi - lo + 3) / 4, lo - skip};
+  const RowPart<false> src{reinterpret_cast<const float4 *>(a.logits + (g0 + lo - skip)),
+                           (skip + hi - lo + 3) / 4, lo - skip, lo, hi};
+  const RowPart<kHeld> r{kHeld ? held : src.z, src.n4, src.index0, lo, hi};
 
   pdl_wait();
   pdl_trigger();
@@ -624,33 +700,30 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
   set.top_p = a.top_p ? a.top_p[row] : 1.f;
   set.min_p = a.min_p ? a.min_p[row] : 0.f;
   const float u0 = a.u[row];
-  float top = -kInf;
-  const float4 *src = reinterpret_cast<const float4 *>(a.logits + (g0 + lo - skip));
-#pragma unroll 8
-  for (int i = tid; i < r.n4; i += kSmThreads) {
-    float4 v;
-    const int e = r.index0 + 4 * i;
-    if (e >= lo && e + 4 <= hi) {
-      v = __ldcs(src + i);
-    } else {
-      const float *z = a.logits + g0 + e;
-      v.x = e >= lo && e < hi ? z[0] : -kInf;
-      v.y = e + 1 >= lo && e + 1 < hi ? z[1] : -kInf;
-      v.z = e + 2 >= lo && e + 2 < hi ? z[2] : -kInf;
-      v.w = e + 3 >= lo && e + 3 < hi ? z[3] : -kInf;
-    }
-    // NaN is never chosen: max(NaN, -inf) is -inf
-    v.x = fmaxf(v.x, -kInf), v.y = fmaxf(v.y, -kInf);
-    v.z = fmaxf(v.z, -kInf), v.w = fmaxf(v.w, -kInf);
-    reinterpret_cast<float4 *>(zs)[i] = v;
-    top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-  }
   set.u = u0 > 0.f ? fmin((double)u0, 1.0) : 0.0;
+  float top = -kInf;
+  for (int i0 = tid; i0 < r.n4; i0 += 8 * kSmThreads) {
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * kSmThreads;
+      v[j] = i < r.n4 ? src.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // NaN is never chosen: max(NaN, -inf) is -inf
+      v[j].x = fmaxf(v[j].x, -kInf), v[j].y = fmaxf(v[j].y, -kInf);
+      v[j].z = fmaxf(v[j].z, -kInf), v[j].w = fmaxf(v[j].w, -kInf);
+      top = fmaxf(top, fmaxf(fmaxf(v[j].x, v[j].y), fmaxf(v[j].z, v[j].w)));
+      if (kHeld && i0 + j * kSmThreads < r.n4) held[i0 + j * kSmThreads] = v[j];
+    }
+  }
   const bool greedy = !(set.T > 0.f) || set.min_p > 1.f || k == 1 || set.top_p <= 0.f;
   const int kk = greedy ? 1 : k;
+  const bool few = kk > 0 && kk <= kSmShort;
 
   // ---- few kept tokens
-  if (kk > 0 && kk <= kSmShort) {
+  if (few) {
     // the largest threshold found that at least kk threads' maxima reach
     const uint32_t mine = zkey(top);
     uint32_t a0 = __reduce_min_sync(0xffffffffu, mine), a1 = __reduce_max_sync(0xffffffffu, mine);
@@ -670,15 +743,10 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
       else end = mid;
     }
     const uint32_t from = max(a0, kNoneKey + 1);
-    if (mine >= from) {
-      for (int i = tid; i < r.n4; i += kSmThreads) {
-        const float4 v = r.z[i];
-        const float z[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (zkey(z[j]) >= from) collect(t, order_key(z[j], r.index0 + 4 * i + j));
-      }
-    }
+    if (mine >= from)
+      r.each([&](float z, int i) {
+        if (z == z && zkey(z) >= from) collect(t, order_key(z, i));
+      });
     cluster_wait();
     hand_over(t);
     t.sync();
@@ -692,7 +760,8 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
   }
   cluster_wait();
 
-  // ---- the general row
+  // ---- the general row, and one with more equal logits than CTA 0 holds
+  if (tid == 0) s.list_n = 0, s.mine_n = 0;
   for (int i = tid; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
   const float M = key_z((uint32_t)t.all_max(zkey(top)));
   if (M == -kInf) {
@@ -700,31 +769,14 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
       a.token[row] = -1;
       if (a.logprob) a.logprob[row] = -kInf;
     }
-    t.sync();
     return;
   }
-  if (greedy) {
-    // (all of a CTA's logits equal or nearly so) the lowest index of M
-    u64 best = 0;
-    for_elements(r, [&](float z, int i) {
-      if (z == M) best = max(best, order_key(z, i));
-    });
-    best = t.all_max(best);
-    if (t.rank == 0 && tid == 0) {
-      a.token[row] = key_index(best);
-      if (a.logprob) a.logprob[row] = 0.f;
-    }
-    t.sync();
-    return;
-  }
-
-  const Dist dist{M, __fdiv_rn(1.4426950408889634f, set.T)};
-  const bool use_k = k > 0 && k < a.V, use_p = set.top_p < 1.f;
+  const Dist dist{M, __fdiv_rn(1.4426950408889634f, greedy ? 1.f : set.T)};
+  const bool use_k = few || (k > 0 && k < a.V), use_p = !few && set.top_p < 1.f;
   u64 cut = 0;  // kept: (z, index) at or before this in the order
   if (use_k || use_p) {
-    uint32_t far_n = 0;
-    double far_mass = 0;
-    for_elements(r, [&](float z, int) {
+    uint32_t far_n = 0, far_units = 0;
+    r.each([&](float z, int) {
       const float d = dist(z);
       if (d < (float)kSmBins / kSmSteps) {
         float edge;
@@ -733,15 +785,18 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
         atomicAdd(&s.eps[b], Dist::units(d, edge));
       } else if (z > -kInf) {
         ++far_n;
-        far_mass += (double)ex2(-d);
+        far_units += Dist::far_units(d);  // up to 2^13 each, 2^9 elements a thread
       }
     });
-    Sum far;
-    t.scan(far_n, far_mass, &far);
-    const int fp = t.exchange(far.c, far.m);
+    long long far_c, far_u;
+    t.scan((long long)far_n, &far_c);
+    t.scan((long long)far_units, &far_u);
+    const int fp = t.post((u64)far_c, (u64)far_u);
     merge_bins(t, [](int b) { return b; });
-    far = {0, 0.0};
-    for (int i = 0; i < t.size; ++i) far.c += (uint32_t)s.slot[fp][i].a, far.m += s.slot[fp][i].b;
+    Sum far{0, 0.0};
+    u64 fu = 0;
+    for (int i = 0; i < t.size; ++i) far.c += (uint32_t)s.slot[fp][i].a, fu += s.slot[fp][i].b;
+    far.m = Dist::mass(far.c, fu, kSmBins);
     const uint32_t bc[2] = {s.tcnt[2 * tid], s.tcnt[2 * tid + 1]};
     const double bm[2] = {s.tmass[2 * tid], s.tmass[2 * tid + 1]};
     Sum all;
@@ -757,8 +812,8 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
       return resolve(t, r, dist, kSmBins, far.c, all.c, all.m, g);
     };
     double mass = all.m + far.m;
-    if (use_k && (uint32_t)k < all.c + far.c) {
-      const Cut c = search(Goal{true, (uint32_t)k, 0.0});
+    if (use_k && (uint32_t)kk < all.c + far.c) {
+      const Cut c = search(Goal{true, (uint32_t)kk, 0.0});
       cut = c.key;
       mass = c.mass;
     }
@@ -766,6 +821,18 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
       const Cut c = search(Goal{false, 0, (double)set.top_p * mass});
       if (c.key > cut) cut = c.key;
     }
+  }
+  if (few) {
+    r.each([&](float z, int i) {
+      if (z > -kInf) {
+        const u64 x = order_key(z, i);
+        if (x >= cut) collect(t, x);
+      }
+    });
+    hand_over(t);
+    t.sync();
+    if (t.rank == 0) finish_short(t, a, row, min((int)s.list_n, kSmList), kk, greedy, set);
+    return;
   }
   if (set.min_p > 0.f) {
     const u64 c = (u64)zkey(min_p_logit(M, set)) << 32;
@@ -781,90 +848,128 @@ __global__ void __launch_bounds__(kSmThreads, 2) k_sample(const __grid_constant_
     return kept ? dist.p(z) : 0.f;
   };
   const int chunks = (r.n4 + 31) / 32;  // at most kSmChunks
-  for (int c = warp; c < chunks; c += kSmWarps) {
-    const int i = 32 * c + lane, e = r.index0 + 4 * i;
-    float x = 0.f;
-    if (i < r.n4) {
-      const float4 v = r.z[i];
-      x = (p_of(v.x, e) + p_of(v.y, e + 1)) + (p_of(v.z, e + 2) + p_of(v.w, e + 3));
+  constexpr int kAhead = RowPart<kHeld>::kAhead;
+  for (int c0 = warp; c0 < chunks; c0 += kAhead * kSmWarps) {
+    float4 v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = 32 * (c0 + j * kSmWarps) + lane;
+      v[j] = i < r.n4 ? r.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) s.chunk[c] = x;
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = c0 + j * kSmWarps, e = r.index0 + 4 * (32 * c + lane);
+      uint32_t uh = 0, ul = 0;
+      Dist::add_units(p_of(v[j].x, e), uh, ul);
+      Dist::add_units(p_of(v[j].y, e + 1), uh, ul);
+      Dist::add_units(p_of(v[j].z, e + 2), uh, ul);
+      Dist::add_units(p_of(v[j].w, e + 3), uh, ul);
+      uh = __reduce_add_sync(0xffffffffu, uh);
+      ul = __reduce_add_sync(0xffffffffu, ul);
+      if (lane == 0 && c < chunks) s.chunk[c] = Dist::whole(uh, ul, kSmChunk);
+    }
   }
   __syncthreads();
-  const double w = tid < chunks ? (double)s.chunk[tid] : 0.0;
-  Sum mine;
-  const Sum at = t.scan(0, w, &mine);
-  const int q = t.exchange(0, mine.m);
-  double total = 0;
-  for (int i = 0; i < t.size; ++i) total += s.slot[q][i].b;
-  const double goal = set.u * total;
-  // the CTA, then the piece, whose running mass passes the goal; the last one
-  // with any mass if none does (u = 1, or the last bit of a sum)
-  int cta = -1;
-  double run = 0, start = 0;
-  for (int i = 0; i < t.size; ++i) {
-    const double x = s.slot[q][i].b;
-    if (x > 0) {
-      cta = i, start = run;
-      if (run + x > goal) break;
-    }
-    run += x;
+  // a thread has `per` pieces next to each other
+  const int per = (chunks + kSmThreads - 1) / kSmThreads;
+  const int c_lo = min(chunks, tid * per), c_hi = min(chunks, c_lo + per);
+  long long w = 0, mine;
+  for (int c = c_lo; c < c_hi; ++c) w += s.chunk[c];
+  const long long at = t.scan(w, &mine);
+  const int q = t.post((u64)mine, 0);
+  t.sync();
+  long long total = 0;
+  for (int i = 0; i < t.size; ++i) total += (long long)s.slot[q][i].a;
+  if (set.u >= 1.0) {
+    // the last kept token, however small its share
+    u64 last = 0;
+    r.each([&](float z, int i) {
+      if (p_of(z, i) > 0.f) last = max(last, ((u64)(i + 1) << 32) | zkey(z));
+    });
+    last = t.all_max(last);
+    if (t.rank == 0 && tid == 0)
+      write_token(a, row, (int)(last >> 32) - 1, key_z((uint32_t)last), M, set.T, total);
+    return;
   }
-  if (cta == t.rank) {
-    if (tid == 0) s.found = 0x7fffffff, s.mine_n = 0;
-    __syncthreads();
-    if (w > 0) {
-      atomicMax(&s.mine_n, (uint32_t)tid);  // the last piece with mass
-      if (start + at.m + w > goal) atomicMin(&s.found, tid);
+  const double goal = set.u * (double)total;
+  // the CTA, then the piece, then the element whose running mass passes the
+  // goal (u < 1: one does)
+  int cta = 0;
+  long long start = 0;
+  for (; cta < t.size - 1; ++cta) {
+    const long long x = (long long)s.slot[q][cta].a;
+    if ((double)(start + x) > goal) break;
+    start += x;
+  }
+  if (cta != t.rank) return;  // (nobody reads another CTA's memory any more)
+  if (tid == 0) s.found = chunks - 1;
+  __syncthreads();
+  long long x = start + at;
+  for (int c = c_lo; c < c_hi; ++c) {
+    x += s.chunk[c];
+    if ((double)x > goal) {
+      atomicMin(&s.found, c);
+      break;
     }
-    __syncthreads();
-    const int c = s.found == 0x7fffffff ? (int)s.mine_n : s.found;
-    if (tid == c) s.at_mass = start + at.m;
-    __syncthreads();
-    if (warp == 0) {
-      const int i = 32 * c + lane, e = r.index0 + 4 * i;
-      float p[4] = {0.f, 0.f, 0.f, 0.f};
-      if (i < r.n4) {
-        const float4 v = r.z[i];
-        p[0] = p_of(v.x, e), p[1] = p_of(v.y, e + 1), p[2] = p_of(v.z, e + 2), p[3] = p_of(v.w, e + 3);
-      }
-      const double own = ((double)p[0] + p[1]) + ((double)p[2] + p[3]);
-      double inc = own;
+  }
+  __syncthreads();
+  const int c = s.found;
+  if (c >= c_lo && c < c_hi) {
+    x = start + at;
+    for (int i = c_lo; i < c; ++i) x += s.chunk[i];
+    s.at_sum = x;
+  }
+  __syncthreads();
+  if (warp) return;
+  const int i = 32 * c + lane, e = r.index0 + 4 * i;
+  float z[4] = {-kInf, -kInf, -kInf, -kInf};
+  if (i < r.n4) {
+    const float4 v = r.load(i);
+    z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
+  }
+  long long own[4], sum = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      double x = s.at_mass + (inc - own);
-      int hit = -1, last = -1;  // row indices
-      for (int j = 0; j < 4; ++j) {
-        x += p[j];
-        if (p[j] > 0.f) {
-          last = e + j;
-          if (hit < 0 && x > goal) hit = last;
-        }
-      }
-      const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0);
-      const uint32_t lasts = __ballot_sync(0xffffffffu, last >= 0);
-      hit = hits ? __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1)
-                 : __shfl_sync(0xffffffffu, last, lasts ? 31 - __clz(lasts) : 0);
-      if (lane == 0) write_token(a, row, hit, hit >= 0 ? zs[hit - r.index0] : M, M, set.T, total);
-    }
+  for (int j = 0; j < 4; ++j) {
+    uint32_t uh = 0, ul = 0;
+    Dist::add_units(p_of(z[j], e + j), uh, ul);
+    own[j] = Dist::whole(uh, ul, 1);
+    sum += own[j];
   }
-  t.sync();  // no CTA leaves while another may still read its memory
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  x = s.at_sum + inc - sum;
+  int hit = -1;  // of this lane's four
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x += own[j];
+    if (hit < 0 && (double)x > goal) hit = j;
+  }
+  const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0);
+  if (hits && lane == __ffs(hits) - 1)
+    write_token(a, row, e + hit, hit == 0 ? z[0] : hit == 1 ? z[1] : hit == 2 ? z[2] : z[3], M,
+                set.T, total);
 }
 
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st) {
-  int size = 1;
-  while (size < kSmMaxCluster && a.V > 2048 * size) size *= 2;
-  const int part = ((a.V + size - 1) / size + 3) & ~3;
-  const size_t smem = (sizeof(SampleShared) + 15) / 16 * 16 + (size_t)(part + 4) * 4;
-  note_step("sample attribute");
-  int dev = 0;
+  int dev = 0, sms = 0;
+  note_step("sample device query");
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = smem_once<k_sample>(dev, 200 * 1024);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // As many CTAs a row as leave every SM at most one (a cluster does not fill
+  // the last SMs of a GPC: an eighth less), and not so many that they have
+  // little to do (a cluster's exchanges cost about 1 us each).
+  int size = 1;
+  while (size < kSmMaxCluster && a.V > 2048 * size && 2 * size * a.B <= sms / 8 * 7) size *= 2;
+  const int part = ((a.V + size - 1) / size + 3) & ~3;
+  const bool held = (size_t)(part + 4) * 4 <= kSmHold;
+  const size_t smem = (sizeof(SampleShared) + 15) / 16 * 16 + (held ? (size_t)(part + 4) * 4 : 0);
+  note_step("sample attribute");
+  e = held ? smem_once<k_sample<true>>(dev, 220 * 1024) : smem_once<k_sample<false>>(dev, 64 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.B * size);
@@ -881,7 +986,8 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   note_step("sample launch");
-  return cudaLaunchKernelEx(&cfg, k_sample, a);
+  return held ? cudaLaunchKernelEx(&cfg, k_sample<true>, a)
+              : cudaLaunchKernelEx(&cfg, k_sample<false>, a);
 }
 
 }  // namespace flint
