@@ -25,8 +25,8 @@
 //      equal logits) are narrowed down by bins of the key in the cluster first;
 //   4. the kept mass in index order, p in units of 2^-44, by pieces of 128
 //      elements, and the token whose running mass passes u times the total.
-// Sums over many elements are integers, and the few in floating point go over
-// the order or the bins: a row's result is the same for every run, batch,
+// All sums are of integers, or of doubles that are multiples of one power of
+// two and exact: a row's result is the same for every run, batch,
 // cluster size and alignment.
 #include <algorithm>
 
@@ -35,11 +35,11 @@
 
 namespace flint {
 
-constexpr int kSmThreads = 512;
-constexpr int kSmWarps = kSmThreads / 32;
+constexpr int kSmMaxThreads = 1024;
 constexpr int kSmBins = 1024;       // steps of 1/32 in log2 units: d < 32
 constexpr float kSmSteps = 32.f;
 constexpr int kSmList = 2048;       // elements gathered in one CTA
+constexpr int kSmSubBits = 9, kSmSub = 1 << kSmSubBits;  // bins of a list's keys
 constexpr int kSmOrder = 128;       // elements put in order at once
 constexpr int kSmShort = 256;       // largest k of the short path
 constexpr int kSmMaxCluster = 8;
@@ -63,14 +63,14 @@ struct SampleShared {
   };
   u64 list[kSmList];
   u64 sorted[kSmShort], mine[kSmShort];
-  uint32_t scnt[kSmThreads], seps[kSmThreads];
+  uint32_t scnt[kSmSub], seps[kSmSub];
   // one exchange between the CTAs uses one of two sets of slots, in turn
   struct {
     u64 a, b;
   } slot[2][kSmMaxCluster];
-  uint32_t red_c[kSmWarps];
-  u64 red_a[kSmWarps];
-  double red_b[kSmWarps];
+  uint32_t red_c[kSmMaxThreads / 32];
+  u64 red_a[kSmMaxThreads / 32];
+  double red_b[kSmMaxThreads / 32];
   u64 res_key[2];
   double res_mass[2];
   uint32_t list_n, mine_n;
@@ -78,6 +78,7 @@ struct SampleShared {
   uint32_t at_n, at_above;
   double at_mass;
   long long at_sum;
+  float bin_lo, bin_hi;
 };
 
 // (below 2^-126: 0)
@@ -101,7 +102,7 @@ FLINT_DEV int key_index(u64 k) { return (int)(0xffffffffu - (uint32_t)k); }
 // [lo, hi) are the CTA's (the pieces are 16 bytes of memory, so the first may
 // start up to 3 elements early and the last end late; those read as -inf).
 // kHeld: in shared memory, where NaN reads as -inf too.
-template <bool kHeld>
+template <bool kHeld, int kT>
 struct RowPart {
   const float4 *z;
   int n4;
@@ -119,25 +120,53 @@ struct RowPart {
     v.w = e + 3 >= lo && e + 3 < hi ? p[3] : kNone;
     return v;
   }
-  static constexpr int kAhead = kHeld ? 2 : 8;
+  static constexpr int kAhead = kHeld ? 2 : 4;
   // f(logit, row index) for this thread's elements
   template <typename F>
   FLINT_DEV void each(F f) const {
     const float kNone = -__int_as_float(0x7f800000);
-    for (int i0 = threadIdx.x; i0 < n4; i0 += kAhead * kSmThreads) {
+    for (int i0 = threadIdx.x; i0 < n4; i0 += kAhead * kT) {
       float4 v[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u * kSmThreads;
+        const int i = i0 + u * kT;
         v[u] = i < n4 ? load(i) : make_float4(kNone, kNone, kNone, kNone);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int e = index0 + 4 * (i0 + u * kSmThreads);
+        const int e = index0 + 4 * (i0 + u * kT);
         f(v[u].x, e);
         f(v[u].y, e + 1);
         f(v[u].z, e + 2);
         f(v[u].w, e + 3);
+      }
+    }
+  }
+  // act(logit, row index) for those of them that test(logit) holds of: few.
+  // The tests of a batch go into a mask, so that act stands in the code once
+  // (unrolled 32 times it cost more than the pass over the row).
+  template <typename P, typename F>
+  FLINT_DEV void find(P test, F act) const {
+    const float kNone = -__int_as_float(0x7f800000);
+    for (int i0 = threadIdx.x; i0 < n4; i0 += kAhead * kT) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kT;
+        v[u] = i < n4 ? load(i) : make_float4(kNone, kNone, kNone, kNone);
+      }
+      uint32_t hits = 0;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        hits |= test(v[u].x) ? 1u << (4 * u) : 0u;
+        hits |= test(v[u].y) ? 2u << (4 * u) : 0u;
+        hits |= test(v[u].z) ? 4u << (4 * u) : 0u;
+        hits |= test(v[u].w) ? 8u << (4 * u) : 0u;
+      }
+#pragma unroll 1
+      for (; hits; hits &= hits - 1) {
+        const int j = __ffs(hits) - 1, at = 4 * (i0 + (j >> 2) * kT) + (j & 3);
+        act(reinterpret_cast<const float *>(z)[at], index0 + at);
       }
     }
   }
@@ -165,7 +194,9 @@ struct Dist {
     const float e = y * fmaf(y, fmaf(y, 1.f / 6, -0.5f), 1.f);
     return __float_as_uint(fmaf(e, kEpsUnit, 8388608.f)) & 0x7fffffu;
   }
-  FLINT_DEV static uint32_t far_units(float d) { return (uint32_t)(ex2(-d) * kFarUnit + 0.5f); }
+  FLINT_DEV static uint32_t far_units(float d) {
+    return __float_as_uint(fmaf(ex2(-d), kFarUnit, 8388608.f)) & 0x7fffffu;
+  }
   // p <= 1 in units of 2^-44, as hi 2^22 + lo, added to the sums of both: hi
   // is p to the nearest 2^-22 (adding 2^23 leaves it in the low bits), lo what
   // that rounded off.  The constants in the bits go out at the end (whole).
@@ -184,21 +215,15 @@ struct Dist {
   }
   // the mass that a count and such a sum stand for
   FLINT_DEV static double mass(u64 n, u64 units, int b) {
-    if (b == kSmBins) return (double)units / kFarUnit;
-    return exp2(-(double)b / kSmSteps) * ((double)n - (double)units / kEpsUnit);
+    if (b == kSmBins) return rounded((double)units / kFarUnit);
+    return rounded(exp2(-(double)b / kSmSteps) * ((double)n - (double)units / kEpsUnit));
+  }
+  // to a multiple of 2^-33: sums of these up to 2^19 are exact in any order
+  FLINT_DEV static double rounded(double x) {
+    const double kBig = 786432.0;  // 1.5 x 2^19
+    return (x + kBig) - kBig;
   }
 };
-// The elements of bin b, by the distances it spans (b / 32 is exact)
-struct InBin {
-  float lo, hi;
-  bool far;
-  FLINT_DEV explicit InBin(int b)
-      : lo((float)b / kSmSteps), hi((float)(b + 1) / kSmSteps), far(b == kSmBins) {}
-  FLINT_DEV bool operator()(float d, float z) const {
-    return d >= lo && (far ? z > -__int_as_float(0x7f800000) : d < hi);
-  }
-};
-
 FLINT_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 FLINT_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -215,7 +240,9 @@ struct Sum {
   double m;
 };
 
+template <int kT>
 struct Team {
+
   SampleShared *s;
   int rank, size, parity = 0, resolved = 0;
   FLINT_DEV void sync() {
@@ -235,7 +262,7 @@ struct Team {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s->red_a[threadIdx.x >> 5] = a;
     __syncthreads();
-    for (int i = 0; i < kSmWarps; ++i) a = a > s->red_a[i] ? a : s->red_a[i];
+    for (int i = 0; i < kT / 32; ++i) a = a > s->red_a[i] ? a : s->red_a[i];
     return a;
   }
   // Sums before each thread's, of integers that fit 63 bits
@@ -251,7 +278,7 @@ struct Team {
     if (lane == 31) s->red_a[w] = (u64)inc;
     __syncthreads();
     long long before = 0, all = 0;
-    for (int i = 0; i < kSmWarps; ++i) {
+    for (int i = 0; i < kT / 32; ++i) {
       if (i == w) before = all;
       all += (long long)s->red_a[i];
     }
@@ -273,7 +300,7 @@ struct Team {
     if (lane == 31) s->red_c[w] = ic, s->red_b[w] = im;
     __syncthreads();
     Sum before{0, 0.0}, all{0, 0.0};
-    for (int i = 0; i < kSmWarps; ++i) {
+    for (int i = 0; i < kT / 32; ++i) {
       if (i == w) before = all;
       all.c += s->red_c[i], all.m += s->red_b[i];
     }
@@ -337,8 +364,8 @@ struct Range {
 // The bin in which a goal is reached, from the block's scan of kPer bins a
 // thread (before: the sums in front of the thread's bins); every thread gets
 // it with its sums, -1 if the bins do not reach the goal.
-template <int kPer>
-FLINT_DEV int pick(Team &t, const Goal &g, const uint32_t (&c)[kPer], const double (&m)[kPer],
+template <int kPer, int kT>
+FLINT_DEV int pick(Team<kT> &t, const Goal &g, const uint32_t (&c)[kPer], const double (&m)[kPer],
                    const Sum &before, uint32_t *n, uint32_t *above, double *mass) {
   SampleShared &s = *t.s;
   __syncthreads();
@@ -367,12 +394,14 @@ FLINT_DEV int pick(Team &t, const Goal &g, const uint32_t (&c)[kPer], const doub
 // An element for CTA 0's list.  The others keep theirs in their own list until
 // hand_over sends them together: a thread that adds to CTA 0's counter waits
 // for the answer through the cluster.  What does not fit is counted only.
-FLINT_DEV void collect(Team &t, u64 key) {
+template <int kT>
+FLINT_DEV void collect(Team<kT> &t, u64 key) {
   SampleShared &s = *t.s;
   const uint32_t at = atomicAdd(t.rank ? &s.mine_n : &s.list_n, 1u);
   if (at < (uint32_t)kSmList) s.list[at] = key;
 }
-FLINT_DEV void hand_over(Team &t) {
+template <int kT>
+FLINT_DEV void hand_over(Team<kT> &t) {
   SampleShared &s = *t.s;
   __syncthreads();
   if (t.rank == 0) return;
@@ -381,20 +410,21 @@ FLINT_DEV void hand_over(Team &t) {
   __syncthreads();
   const uint32_t base = s.at_n;
   u64 *list = t.of(&s.list[0], 0);
-  for (uint32_t i = threadIdx.x; i < n && base + i < (uint32_t)kSmList; i += kSmThreads)
+  for (uint32_t i = threadIdx.x; i < n && base + i < (uint32_t)kSmList; i += kT)
     list[base + i] = s.list[i];
   if (threadIdx.x == 0) s.mine_n = 0;
 }
 
 // The cut among the m elements in this CTA's list, all of bin b (one CTA).
-FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, const Goal &goal) {
+template <int kT>
+FLINT_DEV Cut resolve_list(Team<kT> &t, const Dist &dist, int b, int m, Range r, const Goal &goal) {
   SampleShared &s = *t.s;
   const int tid = threadIdx.x;
   while (r.n > (uint32_t)kSmOrder) {
-    s.scnt[tid] = 0, s.seps[tid] = 0;
+    if (tid < kSmSub) s.scnt[tid] = 0, s.seps[tid] = 0;
     __syncthreads();
-    const int sh = r.shift(9);
-    for (int i = tid; i < m; i += kSmThreads) {
+    const int sh = r.shift(kSmSubBits);
+    for (int i = tid; i < m; i += kT) {
       const u64 k = s.list[i];
       if (k >= r.lo && k <= r.hi) {
         const int x = (int)((r.hi - k) >> sh);
@@ -403,8 +433,8 @@ FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, con
       }
     }
     __syncthreads();
-    const uint32_t c[1] = {s.scnt[tid]};
-    const double ms[1] = {Dist::mass(c[0], s.seps[tid], b)};
+    const uint32_t c[1] = {tid < kSmSub ? s.scnt[tid] : 0u};
+    const double ms[1] = {c[0] ? Dist::mass(c[0], s.seps[tid], b) : 0.0};
     Sum total;
     Sum before = t.scan(c[0], ms[0], &total);
     before.c += r.above, before.m += r.mass_above;
@@ -420,7 +450,7 @@ FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, con
   // the last few, in order
   if (tid == 0) s.mine_n = 0;
   __syncthreads();
-  for (int i = tid; i < m; i += kSmThreads) {
+  for (int i = tid; i < m; i += kT) {
     const u64 k = s.list[i];
     if (k >= r.lo && k <= r.hi) {
       const uint32_t at = atomicAdd(&s.mine_n, 1u);
@@ -438,7 +468,7 @@ FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, con
   __syncthreads();
   const u64 k = tid < n ? s.sorted[tid] : 0;
   const uint32_t c[1] = {tid < n ? 1u : 0u};
-  const double p[1] = {tid < n ? (double)dist.p(key_z((uint32_t)(k >> 32))) : 0.0};
+  const double p[1] = {tid < n ? Dist::rounded(dist.p(key_z((uint32_t)(k >> 32)))) : 0.0};
   Sum total;
   Sum before = t.scan(c[0], p[0], &total);
   before.c += r.above, before.m += r.mass_above;
@@ -447,17 +477,50 @@ FLINT_DEV Cut resolve_list(Team &t, const Dist &dist, int b, int m, Range r, con
   int x = pick<1>(t, goal, c, p, before, &x_n, &x_above, &x_mass);
   if (x < 0) x = pick<1>(t, Goal{true, r.above + total.c, 0.0}, c, p, before, &x_n, &x_above, &x_mass);
   const u64 key = n ? s.sorted[x] : 0;
-  return {key, n ? x_mass + (double)dist.p(key_z((uint32_t)(key >> 32))) : r.mass_above};
+  return {key, n ? x_mass + Dist::rounded(dist.p(key_z((uint32_t)(key >> 32)))) : r.mass_above};
+}
+
+// The logits of bin b, as an interval: two comparisons an element where the
+// distance and its own take ten instructions.  The distance falls with the
+// logit's key, so that both ends are found by a search over keys, 32 at once.
+struct InBin {
+  float lo, hi;
+  FLINT_DEV bool operator()(float z) const { return (z >= lo) & (z <= hi); }
+};
+template <int kT>
+FLINT_DEV InBin in_bin(Team<kT> &t, const Dist &dist, int b) {
+  SampleShared &s = *t.s;
+  if (threadIdx.x < 32) {
+    // the first key nearer than `bound` (M's at the latest)
+    auto nearer = [&](float bound) {
+      uint32_t a = kNoneKey + 1, e = zkey(dist.M);
+      while (a < e) {
+        const uint32_t step = (e - a) / 32 + 1;
+        const u64 k = a + (u64)step * threadIdx.x;
+        const uint32_t yes = __ballot_sync(0xffffffffu, k >= e || dist(key_z((uint32_t)k)) < bound);
+        const uint32_t n = yes ? __ffs(yes) - 1 : 32;  // a + (n - 1) step is not
+        const u64 end = a + (u64)step * n;
+        if (end < e) e = (uint32_t)end;
+        if (n) a += step * (n - 1) + 1;
+      }
+      return a;
+    };
+    const uint32_t lo = b == kSmBins ? kNoneKey + 1 : nearer((float)(b + 1) / kSmSteps);
+    const uint32_t hi = b == 0 ? zkey(dist.M) : nearer((float)b / kSmSteps) - 1;
+    if (threadIdx.x == 0) s.bin_lo = key_z(lo), s.bin_hi = key_z(hi);
+  }
+  __syncthreads();
+  return {s.bin_lo, s.bin_hi};
 }
 
 // This CTA's bins summed over the cluster, to every CTA's tcnt and tmass.
 // bin_of(i): the level-0 bin whose units bin i holds.
-template <typename F>
-FLINT_DEV void merge_bins(Team &t, F bin_of) {
+template <int kT, typename F>
+FLINT_DEV void merge_bins(Team<kT> &t, F bin_of) {
   SampleShared &s = *t.s;
   t.sync();  // every CTA's bins are complete
   const int per = kSmBins / t.size;
-  for (int i = threadIdx.x; i < per; i += kSmThreads) {
+  for (int i = threadIdx.x; i < per; i += kT) {
     const int b = t.rank * per + i;
     uint32_t c = 0;
     u64 e = 0;
@@ -472,60 +535,71 @@ FLINT_DEV void merge_bins(Team &t, F bin_of) {
   t.sync();
 }
 
+// A thread's merged bins and the sums in front of them
+template <int kT>
+FLINT_DEV Sum scan_bins(Team<kT> &t, uint32_t (&c)[(kSmBins / kT)], double (&m)[(kSmBins / kT)], Sum *total) {
+  uint32_t cs = 0;
+  double ms = 0;
+#pragma unroll
+  for (int i = 0; i < (kSmBins / kT); ++i) {
+    c[i] = t.s->tcnt[(kSmBins / kT) * threadIdx.x + i], m[i] = t.s->tmass[(kSmBins / kT) * threadIdx.x + i];
+    cs += c[i], ms += m[i];
+  }
+  return t.scan(cs, ms, total);
+}
+
 // The cut inside bin `b`, which holds n elements behind `above` earlier ones
 // with mass `mass_above`.  Every thread of the cluster takes part and gets
 // the same answer.
-template <bool kHeld>
-FLINT_DEV Cut resolve(Team &t, const RowPart<kHeld> &r, const Dist &dist, int b, uint32_t n,
+template <bool kHeld, int kT>
+FLINT_DEV Cut resolve(Team<kT> &t, const RowPart<kHeld, kT> &r, const Dist &dist, int b, uint32_t n,
                       uint32_t above, double mass_above, const Goal &goal) {
   SampleShared &s = *t.s;
   Range g{0, ~0ull, n, above, mass_above};
-  const InBin in(b);
+  const InBin in = in_bin(t, dist, b);
   if (n > (uint32_t)kSmList) {
     u64 lo = ~0ull, hi = 0;
-    r.each([&](float z, int i) {
-      if (in(dist(z), z)) {
-        const u64 k = order_key(z, i);
-        lo = k < lo ? k : lo, hi = k > hi ? k : hi;
-      }
-    });
+    r.find(in,
+           [&](float z, int i) {
+             const u64 k = order_key(z, i);
+             lo = k < lo ? k : lo, hi = k > hi ? k : hi;
+           });
     g.hi = t.all_max(hi);
     g.lo = ~t.all_max(~lo);
     while (g.n > (uint32_t)kSmList) {
       const int sh = g.shift(10);
-      for (int i = threadIdx.x; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
+      for (int i = threadIdx.x; i < kSmBins; i += kT) s.cnt[i] = 0, s.eps[i] = 0;
       __syncthreads();
-      r.each([&](float z, int i) {
-        if (!in(dist(z), z)) return;
-        const u64 k = order_key(z, i);
-        if (k >= g.lo && k <= g.hi) {
-          const int x = (int)((g.hi - k) >> sh);
-          atomicAdd(&s.cnt[x], 1u);
-          atomicAdd(&s.eps[x], dist.units_of(z, b));
-        }
-      });
+      r.find(in,
+             [&](float z, int i) {
+               const u64 k = order_key(z, i);
+               if (k >= g.lo && k <= g.hi) {
+                 const int x = (int)((g.hi - k) >> sh);
+                 atomicAdd(&s.cnt[x], 1u);
+                 atomicAdd(&s.eps[x], dist.units_of(z, b));
+               }
+             });
       merge_bins(t, [&](int) { return b; });
-      const int i0 = 2 * threadIdx.x;
-      const uint32_t c[2] = {s.tcnt[i0], s.tcnt[i0 + 1]};
-      const double ms[2] = {s.tmass[i0], s.tmass[i0 + 1]};
+      uint32_t c[(kSmBins / kT)];
+      double ms[(kSmBins / kT)];
       Sum total;
-      Sum before = t.scan(c[0] + c[1], ms[0] + ms[1], &total);
+      Sum before = scan_bins(t, c, ms, &total);
       before.c += g.above, before.m += g.mass_above;
       uint32_t x_n, x_above;
       double x_mass;
-      int x = pick<2>(t, goal, c, ms, before, &x_n, &x_above, &x_mass);
+      int x = pick<kSmBins / kT>(t, goal, c, ms, before, &x_n, &x_above, &x_mass);
       if (x < 0)
-        x = pick<2>(t, Goal{true, g.above + total.c, 0.0}, c, ms, before, &x_n, &x_above, &x_mass);
+        x = pick<kSmBins / kT>(t, Goal{true, g.above + total.c, 0.0}, c, ms, before, &x_n, &x_above,
+                         &x_mass);
       g.narrow(x, sh, x_n, x_above, x_mass);
     }
   }
   // gather into CTA 0, which has the rest to do
-  r.each([&](float z, int i) {
-    if (in(dist(z), z)) {
-      const u64 k = order_key(z, i);
-      if (k >= g.lo && k <= g.hi) collect(t, k);
-    }
-  });
+  r.find(in,
+         [&](float z, int i) {
+           const u64 k = order_key(z, i);
+           if (k >= g.lo && k <= g.hi) collect(t, k);
+         });
   hand_over(t);
   t.sync();
   const int at = t.resolved & 1;  // (a slow CTA may still read the other)
@@ -534,7 +608,7 @@ FLINT_DEV Cut resolve(Team &t, const RowPart<kHeld> &r, const Dist &dist, int b,
     const int m = min((int)s.list_n, kSmList);
     if (n <= (uint32_t)kSmList && m > kSmOrder) {
       u64 lo = ~0ull, hi = 0;
-      for (int i = threadIdx.x; i < m; i += kSmThreads) {
+      for (int i = threadIdx.x; i < m; i += kT) {
         const u64 k = s.list[i];
         lo = k < lo ? k : lo, hi = k > hi ? k : hi;
       }
@@ -572,7 +646,8 @@ FLINT_DEV void write_token(const SampleArgs &a, int row, int token, float z, flo
 
 // The rest of a short row, in the one CTA whose list holds its m candidates,
 // the first k of the order among them.
-FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k, bool greedy,
+template <int kT>
+FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, int k, bool greedy,
                             const Settings &p) {
   SampleShared &s = *t.s;
   const int tid = threadIdx.x;
@@ -585,7 +660,7 @@ FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k,
     return;
   }
   u64 hi = 0, lo = ~0ull;
-  for (int i = tid; i < m; i += kSmThreads) {
+  for (int i = tid; i < m; i += kT) {
     const u64 x = s.list[i];
     lo = x < lo ? x : lo, hi = x > hi ? x : hi;
   }
@@ -609,7 +684,7 @@ FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k,
   }
   if (tid == 0) s.mine_n = 0;
   __syncthreads();
-  for (int i = tid; i < m; i += kSmThreads) {
+  for (int i = tid; i < m; i += kT) {
     const u64 x = s.list[i];
     if (x >= from) s.mine[atomicAdd(&s.mine_n, 1u)] = x;  // at most kSmShort
   }
@@ -625,10 +700,10 @@ FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k,
   const int K = min(k, n);
   u64 x = tid < K ? s.sorted[tid] : 0;
   const float z = key_z((uint32_t)(x >> 32));
-  double w = tid < K ? (double)dist.p(z) : 0.0;
+  const float pz = tid < K ? dist.p(z) : 0.f;
   Sum total;
-  Sum before = t.scan(0, w, &total);
-  bool kept = w > 0;
+  Sum before = t.scan(0, Dist::rounded(pz), &total);
+  bool kept = pz > 0.f;
   if (p.top_p < 1.f) kept &= before.m < (double)p.top_p * total.m;
   if (p.min_p > 0.f) kept &= z >= min_p_logit(M, p);
   if (tid == 0) kept = true;  // the first one always
@@ -662,12 +737,12 @@ FLINT_DEV void finish_short(Team &t, const SampleArgs &a, int row, int m, int k,
   if (tid == s.found) write_token(a, row, key_index(x), key_z((uint32_t)(x >> 32)), M, p.T, sum);
 }
 
-template <bool kHeld>
-__global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ SampleArgs a) {
+template <bool kHeld, int kT>
+__global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) unsigned char smraw[];
   SampleShared &s = *reinterpret_cast<SampleShared *>(smraw);
   float4 *held = reinterpret_cast<float4 *>(smraw + (sizeof(SampleShared) + 15) / 16 * 16);
-  Team t;
+  Team<kT> t;
   t.s = &s;
   {
     uint32_t x;
@@ -687,9 +762,9 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
   const int lo = min(a.V, t.rank * part), hi = min(a.V, lo + part);
   const int64_t g0 = (int64_t)row * a.stride;
   const int skip = (int)((g0 + lo) & 3);
-  const RowPart<false> src{reinterpret_cast<const float4 *>(a.logits + (g0 + lo - skip)),
+  const RowPart<false, kT> src{reinterpret_cast<const float4 *>(a.logits + (g0 + lo - skip)),
                            (skip + hi - lo + 3) / 4, lo - skip, lo, hi};
-  const RowPart<kHeld> r{kHeld ? held : src.z, src.n4, src.index0, lo, hi};
+  const RowPart<kHeld, kT> r{kHeld ? held : src.z, src.n4, src.index0, lo, hi};
 
   pdl_wait();
   pdl_trigger();
@@ -702,20 +777,20 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
   const float u0 = a.u[row];
   set.u = u0 > 0.f ? fmin((double)u0, 1.0) : 0.0;
   float top = -kInf;
-  for (int i0 = tid; i0 < r.n4; i0 += 8 * kSmThreads) {
-    float4 v[8];
+  for (int i0 = tid; i0 < r.n4; i0 += 4 * kT) {
+    float4 v[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j * kSmThreads;
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kT;
       v[j] = i < r.n4 ? src.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       // NaN is never chosen: max(NaN, -inf) is -inf
       v[j].x = fmaxf(v[j].x, -kInf), v[j].y = fmaxf(v[j].y, -kInf);
       v[j].z = fmaxf(v[j].z, -kInf), v[j].w = fmaxf(v[j].w, -kInf);
       top = fmaxf(top, fmaxf(fmaxf(v[j].x, v[j].y), fmaxf(v[j].z, v[j].w)));
-      if (kHeld && i0 + j * kSmThreads < r.n4) held[i0 + j * kSmThreads] = v[j];
+      if (kHeld && i0 + j * kT < r.n4) held[i0 + j * kT] = v[j];
     }
   }
   const bool greedy = !(set.T > 0.f) || set.min_p > 1.f || k == 1 || set.top_p <= 0.f;
@@ -729,12 +804,12 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
     uint32_t a0 = __reduce_min_sync(0xffffffffu, mine), a1 = __reduce_max_sync(0xffffffffu, mine);
     if (lane == 0) s.red_a[warp] = ((u64)a1 << 32) | a0;
     __syncthreads();
-    for (int i = 0; i < kSmWarps; ++i) {
+    for (int i = 0; i < kT / 32; ++i) {
       a0 = min(a0, (uint32_t)s.red_a[i]);
       a1 = max(a1, (uint32_t)(s.red_a[i] >> 32));
     }
     // all reach a0; fewer than kk reach a1 + 1
-    uint32_t count = kSmThreads;
+    uint32_t count = kT;
     u64 end = (u64)a1 + 1;
     while (end - a0 > 1 && count > (uint32_t)kk + kk / 4 + 2) {
       const uint32_t mid = a0 + (uint32_t)((end - a0) / 2);
@@ -743,10 +818,10 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
       else end = mid;
     }
     const uint32_t from = max(a0, kNoneKey + 1);
+    const float zfrom = key_z(from);
     if (mine >= from)
-      r.each([&](float z, int i) {
-        if (z == z && zkey(z) >= from) collect(t, order_key(z, i));
-      });
+      r.find([&](float z) { return z >= zfrom; },
+             [&](float z, int i) { collect(t, order_key(z, i)); });
     cluster_wait();
     hand_over(t);
     t.sync();
@@ -762,7 +837,7 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
 
   // ---- the general row, and one with more equal logits than CTA 0 holds
   if (tid == 0) s.list_n = 0, s.mine_n = 0;
-  for (int i = tid; i < kSmBins; i += kSmThreads) s.cnt[i] = 0, s.eps[i] = 0;
+  for (int i = tid; i < kSmBins; i += kT) s.cnt[i] = 0, s.eps[i] = 0;
   const float M = key_z((uint32_t)t.all_max(zkey(top)));
   if (M == -kInf) {
     if (t.rank == 0 && tid == 0) {
@@ -783,10 +858,11 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
         const int b = Dist::bin(d, &edge);
         atomicAdd(&s.cnt[b], 1u);
         atomicAdd(&s.eps[b], Dist::units(d, edge));
-      } else if (z > -kInf) {
-        ++far_n;
-        far_units += Dist::far_units(d);  // up to 2^13 each, 2^9 elements a thread
       }
+      far_n += (d >= (float)kSmBins / kSmSteps) & (z > -kInf);
+      if ((d >= (float)kSmBins / kSmSteps) & (d < 46.f))
+        far_units += Dist::far_units(d);  // up to 2^13 each, 2^9 elements a thread
+
     });
     long long far_c, far_u;
     t.scan((long long)far_n, &far_c);
@@ -797,16 +873,16 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
     u64 fu = 0;
     for (int i = 0; i < t.size; ++i) far.c += (uint32_t)s.slot[fp][i].a, fu += s.slot[fp][i].b;
     far.m = Dist::mass(far.c, fu, kSmBins);
-    const uint32_t bc[2] = {s.tcnt[2 * tid], s.tcnt[2 * tid + 1]};
-    const double bm[2] = {s.tmass[2 * tid], s.tmass[2 * tid + 1]};
+    uint32_t bc[(kSmBins / kT)];
+    double bm[(kSmBins / kT)];
     Sum all;
-    const Sum before = t.scan(bc[0] + bc[1], bm[0] + bm[1], &all);
+    const Sum before = scan_bins(t, bc, bm, &all);
 
     // the bin a goal falls in, and the cut in it
     auto search = [&](const Goal &g) {
       uint32_t n, above;
       double mass;
-      const int b = pick<2>(t, g, bc, bm, before, &n, &above, &mass);
+      const int b = pick<kSmBins / kT>(t, g, bc, bm, before, &n, &above, &mass);
       if (b >= 0) return resolve(t, r, dist, b, n, above, mass, g);
       if (!far.c) return Cut{0ull, all.m};  // nothing behind the bins: no cut
       return resolve(t, r, dist, kSmBins, far.c, all.c, all.m, g);
@@ -823,12 +899,12 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
     }
   }
   if (few) {
-    r.each([&](float z, int i) {
-      if (z > -kInf) {
-        const u64 x = order_key(z, i);
-        if (x >= cut) collect(t, x);
-      }
-    });
+    const float zc = cut ? key_z((uint32_t)(cut >> 32)) : -kInf;
+    r.find([&](float z) { return (z >= zc) & (z > -kInf); },
+           [&](float z, int i) {
+             const u64 x = order_key(z, i);
+             if (x >= cut) collect(t, x);
+           });
     hand_over(t);
     t.sync();
     if (t.rank == 0) finish_short(t, a, row, min((int)s.list_n, kSmList), kk, greedy, set);
@@ -844,21 +920,21 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
   const uint32_t ic = cut ? 0xffffffffu - (uint32_t)cut : 0x7fffffffu;
   auto p_of = [&](float z, int i) {
     // index at most ic among equals; a bare key's ic wraps to "all"
-    const bool kept = z > zc || (z == zc && (uint32_t)i <= ic);
-    return kept ? dist.p(z) : 0.f;
+    const bool kept = (z > zc) | ((z == zc) & ((uint32_t)i <= ic));
+    return ex2(kept ? -dist(z) : -kInf);  // (no branch)
   };
   const int chunks = (r.n4 + 31) / 32;  // at most kSmChunks
-  constexpr int kAhead = RowPart<kHeld>::kAhead;
-  for (int c0 = warp; c0 < chunks; c0 += kAhead * kSmWarps) {
+  constexpr int kAhead = RowPart<kHeld, kT>::kAhead;
+  for (int c0 = warp; c0 < chunks; c0 += kAhead * (kT / 32)) {
     float4 v[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int i = 32 * (c0 + j * kSmWarps) + lane;
+      const int i = 32 * (c0 + j * (kT / 32)) + lane;
       v[j] = i < r.n4 ? r.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int c = c0 + j * kSmWarps, e = r.index0 + 4 * (32 * c + lane);
+      const int c = c0 + j * (kT / 32), e = r.index0 + 4 * (32 * c + lane);
       uint32_t uh = 0, ul = 0;
       Dist::add_units(p_of(v[j].x, e), uh, ul);
       Dist::add_units(p_of(v[j].y, e + 1), uh, ul);
@@ -871,7 +947,7 @@ __global__ void __launch_bounds__(kSmThreads) k_sample(const __grid_constant__ S
   }
   __syncthreads();
   // a thread has `per` pieces next to each other
-  const int per = (chunks + kSmThreads - 1) / kSmThreads;
+  const int per = (chunks + kT - 1) / kT;
   const int c_lo = min(chunks, tid * per), c_hi = min(chunks, c_lo + per);
   long long w = 0, mine;
   for (int c = c_lo; c < c_hi; ++c) w += s.chunk[c];
@@ -966,14 +1042,16 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st) {
   int size = 1;
   while (size < kSmMaxCluster && a.V > 2048 * size && 2 * size * a.B <= sms / 8 * 7) size *= 2;
   const int part = ((a.V + size - 1) / size + 3) & ~3;
+  // (a part that is read again wants more loads under way: 1,024 threads)
   const bool held = (size_t)(part + 4) * 4 <= kSmHold;
   const size_t smem = (sizeof(SampleShared) + 15) / 16 * 16 + (held ? (size_t)(part + 4) * 4 : 0);
   note_step("sample attribute");
-  e = held ? smem_once<k_sample<true>>(dev, 220 * 1024) : smem_once<k_sample<false>>(dev, 64 * 1024);
+  e = held ? smem_once<k_sample<true, 512>>(dev, 220 * 1024)
+           : smem_once<k_sample<false, 1024>>(dev, 64 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.B * size);
-  cfg.blockDim = dim3(kSmThreads);
+  cfg.blockDim = dim3(held ? 512 : 1024);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -986,8 +1064,8 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   note_step("sample launch");
-  return held ? cudaLaunchKernelEx(&cfg, k_sample<true>, a)
-              : cudaLaunchKernelEx(&cfg, k_sample<false>, a);
+  return held ? cudaLaunchKernelEx(&cfg, k_sample<true, 512>, a)
+              : cudaLaunchKernelEx(&cfg, k_sample<false, 1024>, a);
 }
 
 }  // namespace flint
