@@ -12,7 +12,7 @@
 //     the whole prefix, so that a key is read once for all of them.
 // The tiles of all units form one list, which the CTAs of a persistent kernel
 // share evenly: CTA c takes tiles [c n / N, (c + 1) n / N), whatever the
-// sequences' lengths; an own unit counts one tile more than it has, for its
+// sequences' lengths; an own unit counts two tiles more than it has, for its
 // start and end (loading Q, joining the warps, writing the part), so that a
 // CTA does not get twenty sequences of one tile where another gets one of
 // twenty (256 sequences of 1 to 1,024 keys: 112 us without, 4x the floor).
@@ -30,7 +30,7 @@ namespace flint {
 constexpr int kAtKeys = 64;       // keys of a tile
 constexpr int kAtWarps = 4;       // consumer warps, 16 keys of each tile each
 constexpr int kAtThreads = 32 * (kAtWarps + 1);
-constexpr int kAtVisit = 1;      // tiles that an own unit counts beyond its own
+constexpr int kAtVisit = 2;      // tiles that an own unit counts beyond its own
 constexpr int kAtSmallRows = 16;  // rows of a batch whose prefix needs no tcgen05 tile
 
 // The part of the keys that sequence b's row sees, as 64-key tiles.
@@ -145,7 +145,7 @@ struct AtWalk {
     if (t >= end) return;
     if (kPre) {
       n = ceil_div(a.prefix_len, kAtKeys);
-      unit = (int)(t / n);
+      unit = (int)list_div(t, n);
       in = (int)(t - (long long)unit * n);
       b = unit / a.H, h = unit % a.H;
     } else {
@@ -158,7 +158,7 @@ struct AtWalk {
       b = lo;
       const int len = cum[b + 1] - cum[b];
       const long long r = t - (long long)a.H * cum[b];
-      h = (int)(r / len);
+      h = (int)list_div(r, len);
       n = len - kV;
       in = (int)(r - (long long)h * len) - kV;
       unit = b * a.H + h;
@@ -624,11 +624,11 @@ __global__ void __launch_bounds__(kAtThreads, 2)
 }
 
 // ------------------------------------------------------------------ joining the parts
-// kWarps warps a query row: the parts' maxima and the sink give the base; each
-// warp adds every kWarps-th part's sums and outputs in list order (prefix
-// first), and the warps' are added in order.  One warp where the rows fill the
-// GPU; eight where they do not and a row has many parts (8 sequences of up to
-// 131,072 keys, 37 parts a row: 12 us with one, the loads' latency).
+// kWarps warps a query row; each adds every kWarps-th part in list order
+// (prefix first, the sink before all), moving its base as the maximum grows,
+// and the warps' sums are added in order.  The loads of a row's parts are all
+// that takes time: as many warps a row as one wave of blocks holds (a second
+// wave, or one warp for 18 parts, took 15 us where this takes 5).
 template <int kD, int kWarps>
 __global__ void __launch_bounds__(256)
     k_attn_combine(const __grid_constant__ AttnK a, int own_rows, int grid_own) {
@@ -638,8 +638,8 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % kWarps;
   const int row = (blockIdx.x * 8 + warp) / kWarps;
   const int q_heads = a.G * a.H;
-  if (kWarps < 8 && row >= a.B * q_heads) return;
-  const int b = row / q_heads, head = row % q_heads, h = head / a.G, g = head % a.G;
+  if (kWarps == 1 && row >= a.B * q_heads) return;
+  const int b = min(row / q_heads, a.B - 1), head = row % q_heads, h = head / a.G, g = head % a.G;
   const float kNegInf = -__int_as_float(0x7f800000);
   const bool has = a.lens[b] >= 0;
   // parts of this row: prefix slots [p0, p1), own slots [s0, s1)
@@ -661,53 +661,67 @@ __global__ void __launch_bounds__(256)
     s0 = u + list_cta(tiles, ctas, t + kAtVisit);
     s1 = u + list_cta(tiles, ctas, t + n - 1) + 1;
   }
-  const float sink = a.sinks ? a.sinks[head] * kLog2e : kNegInf;
-  float top = sink;
-  for (int i = p0 + lane; i < p1; i += 32)
-    top = fmaxf(top, ld_cg_f32(&a.ml_pre[(size_t)i * a.pre_rows + pr].x));
-  for (int i = s0 + lane; i < s1; i += 32)
-    top = fmaxf(top, ld_cg_f32(&a.ml_own[(size_t)i * own_rows + g].x));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float base = top == kNegInf ? 0.f : top;
   constexpr int kV = kD / 32;
   float acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-  float sum = w == 0 ? at_ex2(sink - base) : 0.f;
-  auto add = [&](const float2 *mlp, const float *op) {
-    const float m = ld_cg_f32(&mlp->x), l = ld_cg_f32(&mlp->y);
-    const float f = at_ex2(m - base);
-    sum += f * l;
-    if (kV == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(op) + lane);
-      acc[0] += f * v.x, acc[1] += f * v.y, acc[2 % kV] += f * v.z, acc[3 % kV] += f * v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2 *>(op) + lane);
-      acc[0] += f * v.x, acc[1] += f * v.y;
-    }
+  // the sink is one more part, of warp 0
+  float top = a.sinks && w == 0 ? a.sinks[head] * kLog2e : kNegInf;
+  float sum = top == kNegInf ? 0.f : 1.f;
+  // (a sink of NaN or +inf comes out as NaN, as among the keys)
+  if (!(fabsf(top) < __int_as_float(0x7f800000)) && top != kNegInf) sum = top - top;
+  auto add = [&](float m, float l, const float (&v)[kV]) {
+    const float up = fmaxf(top, m), base = up == kNegInf ? 0.f : up;
+    const float f0 = at_ex2(top - base), f = at_ex2(m - base);
+    top = up;
+    sum = sum * f0 + f * l;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = acc[i] * f0 + f * v[i];
   };
-#pragma unroll 4
-  for (int i = p0 + w; i < p1; i += kWarps)
-    add(a.ml_pre + (size_t)i * a.pre_rows + pr, a.o_pre + ((size_t)i * a.pre_rows + pr) * kD);
-#pragma unroll 4
-  for (int i = s0 + w; i < s1; i += kWarps)
-    add(a.ml_own + (size_t)i * own_rows + g, a.o_own + ((size_t)i * own_rows + g) * kD);
+  const int np = p1 - p0, all = np + s1 - s0;
+  constexpr int kAhead = 4;
+  for (int i0 = w; i0 < all; i0 += kAhead * kWarps) {
+    float2 ml[kAhead];
+    float v[kAhead][kV];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * kWarps;
+      if (i < all) {
+        const size_t at = i < np ? (size_t)(p0 + i) * a.pre_rows + pr
+                                 : (size_t)(s0 + i - np) * own_rows + g;
+        ml[u] = __ldcg((i < np ? a.ml_pre : a.ml_own) + at);
+        const float *op = (i < np ? a.o_pre : a.o_own) + at * kD;
+        if (kV == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(op) + lane);
+          v[u][0] = x.x, v[u][1] = x.y, v[u][2 % kV] = x.z, v[u][3 % kV] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2 *>(op) + lane);
+          v[u][0] = x.x, v[u][1] = x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i0 + u * kWarps < all) add(ml[u].x, ml[u].y, v[u]);
+  }
   if (kWarps > 1) {
 #pragma unroll
     for (int i = 0; i < kV; i += 2) part[warp][16 * i + lane] = make_float2(acc[i], acc[i + 1]);
-    if (lane == 0) part[warp][16 * kV].x = sum;
+    if (lane == 0) part[warp][16 * kV] = make_float2(top, sum);
     __syncthreads();
-    if (w) return;
+    if (w || row >= a.B * q_heads) return;
     for (int x = 1; x < kWarps; ++x) {
+      float v[kV];
 #pragma unroll
       for (int i = 0; i < kV; i += 2) {
         const float2 y = part[warp + x][16 * i + lane];
-        acc[i] += y.x, acc[i + 1] += y.y;
+        v[i] = y.x, v[i + 1] = y.y;
       }
-      sum += part[warp + x][16 * kV].x;
+      const float2 ml = part[warp + x][16 * kV];
+      add(ml.x, ml.y, v);
     }
   }
+  const float base = top == kNegInf ? 0.f : top;
   const float vs = a.v_scale ? a.v_scale[h] : 1.f;
   const float inv = sum == 0.f ? 0.f : vs / sum;
   uint16_t *dst = a.out + (int64_t)b * a.out_stride + (int64_t)head * kD;
@@ -851,7 +865,13 @@ cudaError_t launch_attn_as(const flint_kv_cache &c, const CUtensorMap &k, const 
   if (e != cudaSuccess) return e;
   note_step("attention combine launch");
   const int own_rows = a.G <= 8 ? 8 : 16, all = rows * a.H;
-  if (all <= 8 * sms) return at_launch(k_attn_combine<kD, 8>, all, 256, 0, st, a, own_rows, wide);
+  const int wave = 32 * sms;  // warps
+  if (all * 8 <= wave)
+    return at_launch(k_attn_combine<kD, 8>, all, 256, 0, st, a, own_rows, wide);
+  if (all * 4 <= wave)
+    return at_launch(k_attn_combine<kD, 4>, ceil_div(all, 2), 256, 0, st, a, own_rows, wide);
+  if (all * 2 <= wave)
+    return at_launch(k_attn_combine<kD, 2>, ceil_div(all, 4), 256, 0, st, a, own_rows, wide);
   return at_launch(k_attn_combine<kD, 1>, ceil_div(all, 8), 256, 0, st, a, own_rows, wide);
 }
 

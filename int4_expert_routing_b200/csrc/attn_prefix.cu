@@ -123,7 +123,7 @@ struct PreRun {
 };
 FLINT_DEV bool pre_run(const AttnK &a, int n, long long &t, long long t1, PreRun &r) {
   if (t >= t1) return false;
-  r.unit = (int)(t / n);
+  r.unit = (int)list_div(t, n);
   r.j0 = (int)(t - (long long)r.unit * n);
   const long long left = t1 - t;
   r.j1 = left < n - r.j0 ? r.j0 + (int)left : n;
@@ -386,41 +386,50 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
       const bool active = R0 < rows && 128 * x < a.pre_rows, valid = active && R < rows;
       float fac = scale2;
       if (active) {
-        // this row of Q, in the operand's swizzle
-        const int sb = R / a.G, sg = R - sb * a.G;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            a.q + (int64_t)(valid ? sb : 0) * a.q_stride + (int64_t)(r.h * a.G + (valid ? sg : 0)) * kD);
-        unsigned char *q = sm + x * C::kTile + row * 128;
-        uint4 w[kD / 8];
+        // Q, in the operand's swizzle: a warp's 32 rows, whole rows at a time
+        // (a thread's own row took a line for every 16 bytes)
+        constexpr int kPer = kD / 8;               // lanes of a row
+        constexpr int kStep = 32 / kPer;           // rows of a load
+        const int sb = valid ? R / a.G : 0, sg = valid ? R - sb * a.G : 0;
+        const int64_t at = (int64_t)sb * a.q_stride + (int64_t)(r.h * a.G + sg) * kD;
+        uint4 w[kPer];
 #pragma unroll
-        for (int c = 0; c < kD / 8; ++c) w[c] = valid ? src[c] : make_uint4(0, 0, 0, 0);
-        float f1 = 1.f, f2 = 1.f;
-        if (kF8) {
-          fac *= a.k_scale ? a.k_scale[r.h] : 1.f;
-          // the power of two that puts the row's largest element in [2^14, 2^15)
-          uint32_t top = 0;
-#pragma unroll
-          for (int c = 0; c < kD / 8; ++c) {
-            const uint32_t y[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max(y[i] & 0x7fffu, (y[i] >> 16) & 0x7fffu));
-          }
-          const int e = min(max((int)(top >> 7), 1), 254), sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
-          f1 = __uint_as_float((uint32_t)(127 + s1) << 23);
-          f2 = __uint_as_float((uint32_t)(127 + s2) << 23);
-          fac *= __uint_as_float((uint32_t)(127 - s1) << 23);
-          fac *= __uint_as_float((uint32_t)(127 - s2) << 23);
+        for (int i = 0; i < kPer; ++i) {
+          const int from = kStep * i + lane / kPer;
+          const int64_t row_at = __shfl_sync(0xffffffffu, at, from);
+          w[i] = R0 + 32 * (warp & 3) + from < rows
+                     ? reinterpret_cast<const uint4 *>(a.q + row_at)[lane % kPer]
+                     : make_uint4(0, 0, 0, 0);
         }
+        if (kF8) fac *= a.k_scale ? a.k_scale[r.h] : 1.f;
 #pragma unroll
-        for (int c = 0; c < kD / 8; ++c) {
-          uint32_t y[4] = {w[c].x ^ q_sign, w[c].y ^ q_sign, w[c].z ^ q_sign, w[c].w ^ q_sign};
+        for (int i = 0; i < kPer; ++i) {
+          uint32_t y[4] = {w[i].x ^ q_sign, w[i].y ^ q_sign, w[i].z ^ q_sign, w[i].w ^ q_sign};
           if (kF8) {
+            // the power of two that puts the row's largest element in [2^14, 2^15)
+            uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              y[i] = pk_f16(__uint_as_float(y[i] << 16) * f1 * f2,
-                            __uint_as_float(y[i] & 0xffff0000u) * f1 * f2);
+            for (int c = 0; c < 4; ++c) top = max(top, max(y[c] & 0x7fffu, (y[c] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = 1; o < kPer; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = min(max((int)(top >> 7), 1), 254), sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
+            const float f1 = __uint_as_float((uint32_t)(127 + s1) << 23);
+            const float f2 = __uint_as_float((uint32_t)(127 + s2) << 23);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              y[c] = pk_f16(__uint_as_float(y[c] << 16) * f1 * f2,
+                            __uint_as_float(y[c] & 0xffff0000u) * f1 * f2);
+            // it goes out of the scores of the thread that has the row
+            const int mine = __shfl_sync(0xffffffffu, sh, (lane % kStep) * kPer);
+            if (lane / kStep == i) {
+              const int t1_ = mine / 2, t2_ = mine - t1_;
+              fac *= __uint_as_float((uint32_t)(127 - t1_) << 23);
+              fac *= __uint_as_float((uint32_t)(127 - t2_) << 23);
+            }
           }
-          *reinterpret_cast<uint4 *>(q + (c >> 3) * C::kAtom + (((c & 7) ^ (row & 7)) << 4)) =
+          const int qr = 32 * (warp & 3) + kStep * i + lane / kPer, c = lane % kPer;
+          *reinterpret_cast<uint4 *>(sm + x * C::kTile + qr * 128 + (c >> 3) * C::kAtom +
+                                     (((c & 7) ^ (qr & 7)) << 4)) =
               make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
