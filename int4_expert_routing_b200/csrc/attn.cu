@@ -113,7 +113,11 @@ struct AtTile {
   static constexpr int kHalves = kRow / kHalfRow;
   static constexpr int kHalfBytes = kHalfRow * kAtKeys;
   static constexpr int kBytes = kRow * kAtKeys;
-  static constexpr int kStages = kBytes >= 16384 ? 3 : (kBytes >= 8192 ? 6 : 10);
+  // CTAs of an SM, and stages that fill its shared memory.  E4M3 tiles take as
+  // long to compute on as twice the bytes of bf16: a third CTA hides more of it
+  // (64 sequences of 100 to 4,096 keys: 52.9 -> 51.7 us; bf16 loses, 166 -> 173)
+  static constexpr int kCtas = kF8 ? 3 : 2;
+  static constexpr int kStages = kBytes >= 16384 ? 3 : (!kF8 ? 6 : kBytes >= 8192 ? 4 : 8);
   // byte offset of 16-byte chunk c of row r
   static FLINT_DEV uint32_t at(int r, int c) {
     if (kHalfRow == 128)
@@ -211,7 +215,7 @@ struct AtJoin {
 
 // kRows = 8 kNT query rows a unit
 template <int kD, bool kF8, int kNT, bool kPre>
-__global__ void __launch_bounds__(kAtThreads, 2)
+__global__ void __launch_bounds__(kAtThreads, AtTile<kD, kF8>::kCtas)
     k_attn_parts(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ AttnK a) {
   using Tile = AtTile<kD, kF8>;
@@ -641,21 +645,25 @@ __global__ void __launch_bounds__(256)
   if (kWarps == 1 && row >= a.B * q_heads) return;
   const int b = min(row / q_heads, a.B - 1), head = row % q_heads, h = head / a.G, g = head % a.G;
   const float kNegInf = -__int_as_float(0x7f800000);
-  const bool has = a.lens[b] >= 0;
+  // (loaded together: nothing else runs meanwhile)
+  const int len = a.lens[b], c0 = a.cum[b], c1 = a.cum[b + 1], c_all = a.cum[a.B];
+  // the sink is one more part, of warp 0
+  float top = a.sinks && w == 0 ? a.sinks[head] * kLog2e : kNegInf;
+  const float vs = a.v_scale ? a.v_scale[h] : 1.f;
   // parts of this row: prefix slots [p0, p1), own slots [s0, s1)
   int p0 = 0, p1 = 0, s0 = 0, s1 = 0, pr = 0;
-  if (has && a.behind_prefix) {
+  if (a.behind_prefix && len >= 0) {
     const int R = b * a.G + g, blk = R / a.pre_rows;
-    pr = R % a.pre_rows;
-    const int n = ceil_div(a.prefix_len, a.pre_keys), u = blk * a.H + h;
+    pr = R - blk * a.pre_rows;
+    const int n = ceil_div(a.prefix_len, a.pre_keys) + a.pre_visit, u = blk * a.H + h;
     const long long tiles = (long long)ceil_div(a.B * a.G, a.pre_rows) * a.H * n;
     const long long t = (long long)u * n;
-    p0 = u + list_cta(tiles, a.ctas_pre, t);
+    p0 = u + list_cta(tiles, a.ctas_pre, t + a.pre_visit);
     p1 = u + list_cta(tiles, a.ctas_pre, t + n - 1) + 1;
   }
-  const int c0 = a.cum[b], n = a.cum[b + 1] - c0;
+  const int n = c1 - c0;
   if (n > 0) {
-    const long long tiles = (long long)a.H * a.cum[a.B];
+    const long long tiles = (long long)a.H * c_all;
     const int ctas = list_ctas(tiles, grid_own), u = b * a.H + h;
     const long long t = (long long)a.H * c0 + (long long)h * n;
     s0 = u + list_cta(tiles, ctas, t + kAtVisit);
@@ -665,8 +673,6 @@ __global__ void __launch_bounds__(256)
   float acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-  // the sink is one more part, of warp 0
-  float top = a.sinks && w == 0 ? a.sinks[head] * kLog2e : kNegInf;
   float sum = top == kNegInf ? 0.f : 1.f;
   // (a sink of NaN or +inf comes out as NaN, as among the keys)
   if (!(fabsf(top) < __int_as_float(0x7f800000)) && top != kNegInf) sum = top - top;
@@ -722,7 +728,6 @@ __global__ void __launch_bounds__(256)
     }
   }
   const float base = top == kNegInf ? 0.f : top;
-  const float vs = a.v_scale ? a.v_scale[h] : 1.f;
   const float inv = sum == 0.f ? 0.f : vs / sum;
   uint16_t *dst = a.out + (int64_t)b * a.out_stride + (int64_t)head * kD;
   if (kV == 4)
@@ -843,13 +848,14 @@ cudaError_t launch_attn_as(const flint_kv_cache &c, const CUtensorMap &k, const 
                            AttnK &a, int sms, cudaStream_t st) {
   cudaError_t e;
   const int rows = a.B * a.G;
-  const int wide = 2 * sms < kAtMaxCtas ? 2 * sms : kAtMaxCtas;
+  constexpr int kCtas = AtTile<kD, kF8>::kCtas;
+  const int wide = kCtas * sms < kAtMaxCtas ? kCtas * sms : kAtMaxCtas;
   a.behind_prefix = a.prefix_len > 0 && a.window == 0;
   if (a.behind_prefix) {
     if (a.pre_rows <= kAtSmallRows) {
       const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H *
                               ceil_div(a.prefix_len, kAtKeys);
-      a.pre_keys = kAtKeys;
+      a.pre_keys = kAtKeys, a.pre_visit = 0;
       a.ctas_pre = (int)(tiles < wide ? tiles : wide);
       note_step("attention prefix launch");
       e = a.pre_rows == 8 ? launch_parts<kD, kF8, 1, true>(k, v, a, a.ctas_pre, st)

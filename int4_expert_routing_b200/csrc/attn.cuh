@@ -36,6 +36,7 @@ struct AttnK {
   float2 *ml_own, *ml_pre;
   int ctas_pre;              // CTAs of the prefix list
   int pre_rows, pre_keys;    // rows of a prefix unit, keys of its tiles
+  int pre_visit;             // tiles that a prefix unit counts beyond its own
   int dev;
   int behind_prefix;         // the own keys' kernel follows a prefix kernel
 };
@@ -52,13 +53,11 @@ FLINT_DEV long long list_div(long long x, int y) {
 FLINT_DEV long long list_start(long long tiles, int ctas, int c) {
   return list_div(tiles * c, ctas);
 }
-// the CTA that holds tile t
+// the CTA that holds tile t: the last c with tiles c / ctas < t + 1
 FLINT_DEV int list_cta(long long tiles, int ctas, long long t) {
-  const unsigned long long x = (unsigned long long)t * ctas;
-  int c = (x | (unsigned long long)tiles) >> 32 ? (int)(x / tiles) : (int)((uint32_t)x / (uint32_t)tiles);
-  while (c + 1 < ctas && list_start(tiles, ctas, c + 1) <= t) ++c;
-  while (c > 0 && list_start(tiles, ctas, c) > t) --c;
-  return c;
+  const unsigned long long x = (unsigned long long)(t + 1) * ctas - 1;
+  return (x | (unsigned long long)tiles) >> 32 ? (int)(x / tiles)
+                                               : (int)((uint32_t)x / (uint32_t)tiles);
 }
 
 FLINT_DEV float at_ex2(float x) {

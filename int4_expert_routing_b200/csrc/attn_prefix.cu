@@ -122,14 +122,20 @@ struct PreRun {
   int unit, blk, h, j0, j1;
 };
 FLINT_DEV bool pre_run(const AttnK &a, int n, long long &t, long long t1, PreRun &r) {
-  if (t >= t1) return false;
-  r.unit = (int)list_div(t, n);
-  r.j0 = (int)(t - (long long)r.unit * n);
-  const long long left = t1 - t;
-  r.j1 = left < n - r.j0 ? r.j0 + (int)left : n;
-  r.blk = r.unit / a.H, r.h = r.unit % a.H;
-  t += r.j1 - r.j0;
-  return true;
+  while (t < t1) {
+    // places of the list: pre_visit in front of a unit's tiles
+    const int len = n + a.pre_visit;
+    r.unit = (int)list_div(t, len);
+    const int at = (int)(t - (long long)r.unit * len);
+    const long long left = t1 - t;
+    const int end = left < len - at ? at + (int)left : len;
+    t += end - at;
+    r.j0 = max(at - a.pre_visit, 0), r.j1 = end - a.pre_visit;
+    if (r.j1 <= r.j0) continue;
+    r.blk = r.unit / a.H, r.h = r.unit - r.blk * a.H;
+    return true;
+  }
+  return false;
 }
 
 template <int kD, bool kF8>
@@ -177,16 +183,19 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;  // columns: S_A 0, S_B 128, O_A 256, O_B 384
-  pdl_wait();
-  pdl_trigger();
   const int rows = a.B * a.G, n = ceil_div(a.prefix_len, kPkKeys);
-  const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H * n;
+  const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H * (n + a.pre_visit);
   long long t = list_start(tiles, gridDim.x, blockIdx.x);
   const long long t1 = list_start(tiles, gridDim.x, blockIdx.x + 1);
+  // The first unit is worked out in front of the wait for the kernels before
+  // this one: it takes arguments only.
   PreRun r;
+  bool more = pre_run(a, n, t, t1, r);
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegCtl));
+    pdl_wait();
+    pdl_trigger();
     if (warp == 8) {
       // ---- producer: lane i loads box i (of 16 at most) of K, then of V
       constexpr int kRing = kF8 ? C::kRaw : C::kSlots;
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
       unsigned char *ring = kF8 ? raw : slots;
       uint32_t k = 0;
       bool ok = true;
-      while (ok && pre_run(a, n, t, t1, r)) {
+      for (; ok && more; more = pre_run(a, n, t, t1, r)) {
         for (int j = r.j0; j < r.j1 && ok; ++j) {
           const int boxes = ceil_div(min(kPkKeys, a.prefix_len - j * kPkKeys), box_rows);
           const int piece = lane / boxes, x = lane - piece * boxes;
@@ -283,7 +292,7 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
           __syncwarp();
         }
       };
-      while (ok && pre_run(a, n, t, t1, r)) {
+      for (; ok && more; more = pre_run(a, n, t, t1, r)) {
         const int nb = rows - r.blk * a.pre_rows > 128 ? 2 : 1;
         for (int x = 0; x < nb; ++x) wait(&qready[x], nq[x]++ & 1);
         int last_keys = kPkKeys;
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
       const int ct = tid - 384;
       uint32_t k = 0;
       bool ok = true;
-      while (ok && pre_run(a, n, t, t1, r)) {
+      for (; ok && more; more = pre_run(a, n, t, t1, r)) {
         for (int j = r.j0; j < r.j1 && ok; ++j) {
           const int keys = min(kPkKeys, a.prefix_len - j * kPkKeys);
           for (int v = 0; v < 2 && ok; ++v, ++k) {
@@ -375,13 +384,15 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
   } else {
     // ---- softmax: thread = row 32 (warp % 4) + lane of block x
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
+    pdl_wait();
+    pdl_trigger();
     const int x = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
     const float kNegInf = -__int_as_float(0x7f800000);
     uint32_t ns = 0, nu = 0;
     bool ok = true;
-    while (ok && pre_run(a, n, t, t1, r)) {
+    for (; ok && more; more = pre_run(a, n, t, t1, r)) {
       const int R0 = r.blk * a.pre_rows + 128 * x, R = R0 + row;
       const bool active = R0 < rows && 128 * x < a.pre_rows, valid = active && R < rows;
       float fac = scale2;
@@ -392,45 +403,64 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
         constexpr int kStep = 32 / kPer;           // rows of a load
         const int sb = valid ? R / a.G : 0, sg = valid ? R - sb * a.G : 0;
         const int64_t at = (int64_t)sb * a.q_stride + (int64_t)(r.h * a.G + sg) * kD;
-        uint4 w[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int from = kStep * i + lane / kPer;
-          const int64_t row_at = __shfl_sync(0xffffffffu, at, from);
-          w[i] = R0 + 32 * (warp & 3) + from < rows
-                     ? reinterpret_cast<const uint4 *>(a.q + row_at)[lane % kPer]
-                     : make_uint4(0, 0, 0, 0);
-        }
         if (kF8) fac *= a.k_scale ? a.k_scale[r.h] : 1.f;
+        constexpr int kBatch = kF8 ? 4 : 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPer; i0 += kBatch) {
+          uint4 w[kBatch];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          uint32_t y[4] = {w[i].x ^ q_sign, w[i].y ^ q_sign, w[i].z ^ q_sign, w[i].w ^ q_sign};
-          if (kF8) {
-            // the power of two that puts the row's largest element in [2^14, 2^15)
-            uint32_t top = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) top = max(top, max(y[c] & 0x7fffu, (y[c] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = 1; o < kPer; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = min(max((int)(top >> 7), 1), 254), sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
-            const float f1 = __uint_as_float((uint32_t)(127 + s1) << 23);
-            const float f2 = __uint_as_float((uint32_t)(127 + s2) << 23);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              y[c] = pk_f16(__uint_as_float(y[c] << 16) * f1 * f2,
-                            __uint_as_float(y[c] & 0xffff0000u) * f1 * f2);
-            // it goes out of the scores of the thread that has the row
-            const int mine = __shfl_sync(0xffffffffu, sh, (lane % kStep) * kPer);
-            if (lane / kStep == i) {
-              const int t1_ = mine / 2, t2_ = mine - t1_;
-              fac *= __uint_as_float((uint32_t)(127 - t1_) << 23);
-              fac *= __uint_as_float((uint32_t)(127 - t2_) << 23);
-            }
+          for (int i = 0; i < kBatch; ++i) {
+            const int from = kStep * (i0 + i) + lane / kPer;
+            const int64_t row_at = __shfl_sync(0xffffffffu, at, from);
+            w[i] = R0 + 32 * (warp & 3) + from < rows
+                       ? reinterpret_cast<const uint4 *>(a.q + row_at)[lane % kPer]
+                       : make_uint4(0, 0, 0, 0);
           }
-          const int qr = 32 * (warp & 3) + kStep * i + lane / kPer, c = lane % kPer;
-          *reinterpret_cast<uint4 *>(sm + x * C::kTile + qr * 128 + (c >> 3) * C::kAtom +
-                                     (((c & 7) ^ (qr & 7)) << 4)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
+          float f1[kBatch], f2[kBatch];
+          if (kF8) {
+            // the power of two that puts a row's largest element in [2^14, 2^15)
+            // (step by step for the whole batch: a row's own steps wait for
+            // one another)
+            uint32_t top[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              top[i] = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+              top[i] = max(top[i] & 0xffffu, top[i] >> 16);
+            }
+#pragma unroll
+            for (int o = 1; o < kPer; o *= 2)
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i)
+                top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+            int mine = 0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int e = min(max((int)(top[i] >> 7), 1), 254), sh = 141 - e, s1 = sh / 2;
+              f1[i] = __uint_as_float((uint32_t)(127 + s1) << 23);
+              f2[i] = __uint_as_float((uint32_t)(127 + sh - s1) << 23);
+              // it goes out of the scores of the thread that has the row
+              const int from = __shfl_sync(0xffffffffu, sh, (lane % kStep) * kPer);
+              if (lane / kStep == i0 + i) mine = from;
+            }
+            const int s1 = mine / 2;
+            fac *= __uint_as_float((uint32_t)(127 - s1) << 23);
+            fac *= __uint_as_float((uint32_t)(127 - mine + s1) << 23);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            uint32_t y[4] = {w[i].x ^ q_sign, w[i].y ^ q_sign, w[i].z ^ q_sign, w[i].w ^ q_sign};
+            if (kF8) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                y[c] = pk_f16(__uint_as_float(y[c] << 16) * f1[i] * f2[i],
+                              __uint_as_float(y[c] & 0xffff0000u) * f1[i] * f2[i]);
+            }
+            const int qr = 32 * (warp & 3) + kStep * (i0 + i) + lane / kPer, c = lane % kPer;
+            *reinterpret_cast<uint4 *>(sm + x * C::kTile + qr * 128 + (c >> 3) * C::kAtom +
+                                       (((c & 7) ^ (qr & 7)) << 4)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
       }
       if (!active) continue;
@@ -583,10 +613,14 @@ cudaError_t launch_attn_prefix(const flint_kv_cache &c, AttnK &a, int sms, cudaS
   if ((e = pages_map(&k, c, c.k, box_rows)) != cudaSuccess ||
       (e = pages_map(&v, c, c.v, box_rows)) != cudaSuccess)
     return e;
-  const long long tiles = (long long)ceil_div(a.B * a.G, a.pre_rows) * a.H *
-                          ceil_div(a.prefix_len, kPkKeys);
-  const int grid = sms < kAtPreCtas ? sms : kAtPreCtas;
+  const int n = ceil_div(a.prefix_len, kPkKeys), grid = sms < kAtPreCtas ? sms : kAtPreCtas;
+  const long long units = (long long)ceil_div(a.B * a.G, a.pre_rows) * a.H;
   a.pre_keys = kPkKeys;
+  // A unit's start and end (Q in, the part out) take as long as three tiles:
+  // a CTA that has two units' gets fewer tiles, where it has enough of them
+  // (256 sequences on 16,384 keys: 117 us without).
+  a.pre_visit = units * n >= 8LL * grid ? 3 : 0;
+  const long long tiles = units * (n + a.pre_visit);
   a.ctas_pre = (int)(tiles < grid ? tiles : grid);
   note_step("attention prefix launch");
   if (c.head_dim == 128)
