@@ -55,9 +55,9 @@ typedef unsigned long long u64;
 struct SampleShared {
   union {
     struct {
-      uint32_t cnt[kSmBins], eps[kSmBins];  // this CTA's bins
-      uint32_t tcnt[kSmBins];               // the cluster's
-      double tmass[kSmBins];
+      // this CTA's bins and the cluster's; the last is all behind the bins
+      uint32_t cnt[kSmBins + 2], eps[kSmBins + 2], tcnt[kSmBins + 2];
+      double tmass[kSmBins + 2];
     };
     long long chunk[kSmChunks];  // the last step's
   };
@@ -172,6 +172,17 @@ struct RowPart {
   }
 };
 
+// 2^(-i / 32), rounded
+__constant__ double kRoot[32] = {
+    0x1.0000000000000p+0, 0x1.f50765b6e4540p-1, 0x1.ea4afa2a490dap-1, 0x1.dfc97337b9b5fp-1,
+    0x1.d5818dcfba487p-1, 0x1.cb720dcef9069p-1, 0x1.c199bdd85529cp-1, 0x1.b7f76f2fb5e47p-1,
+    0x1.ae89f995ad3adp-1, 0x1.a5503b23e255dp-1, 0x1.9c49182a3f090p-1, 0x1.93737b0cdc5e5p-1,
+    0x1.8ace5422aa0dbp-1, 0x1.82589994cce13p-1, 0x1.7a11473eb0187p-1, 0x1.71f75e8ec5f74p-1,
+    0x1.6a09e667f3bcdp-1, 0x1.6247eb03a5585p-1, 0x1.5ab07dd485429p-1, 0x1.5342b569d4f82p-1,
+    0x1.4bfdad5362a27p-1, 0x1.44e086061892dp-1, 0x1.3dea64c123422p-1, 0x1.371a7373aa9cbp-1,
+    0x1.306fe0a31b715p-1, 0x1.29e9df51fdee1p-1, 0x1.2387a6e756238p-1, 0x1.1d4873168b9aap-1,
+    0x1.172b83c7d517bp-1, 0x1.11301d0125b51p-1, 0x1.0b5586cf9890fp-1, 0x1.059b0d3158574p-1};
+
 struct Dist {
   float M, c;
   // log2 of p(max) / p(z), >= 0; +inf where p = 0 (-inf)
@@ -216,7 +227,10 @@ struct Dist {
   // the mass that a count and such a sum stand for
   FLINT_DEV static double mass(u64 n, u64 units, int b) {
     if (b == kSmBins) return rounded((double)units / kFarUnit);
-    return rounded(exp2(-(double)b / kSmSteps) * ((double)n - (double)units / kEpsUnit));
+    // 2^(-b / 32) = 2^-(b / 32) 2^-(b % 32 / 32)
+    const double first = __longlong_as_double(__double_as_longlong(kRoot[b & 31]) -
+                                              ((long long)(b >> 5) << 52));
+    return rounded(first * ((double)n - (double)units * (1.0 / kEpsUnit)));
   }
   // to a multiple of 2^-33: sums of these up to 2^19 are exact in any order
   FLINT_DEV static double rounded(double x) {
@@ -246,8 +260,12 @@ struct Team {
   SampleShared *s;
   int rank, size, parity = 0, resolved = 0;
   FLINT_DEV void sync() {
-    cluster_arrive();
-    cluster_wait();
+    if (size == 1) {
+      __syncthreads();
+    } else {
+      cluster_arrive();
+      cluster_wait();
+    }
   }
   template <typename T>
   FLINT_DEV T *of(T *p, int r) {
@@ -520,8 +538,8 @@ FLINT_DEV void merge_bins(Team<kT> &t, F bin_of) {
   SampleShared &s = *t.s;
   t.sync();  // every CTA's bins are complete
   const int per = kSmBins / t.size;
-  for (int i = threadIdx.x; i < per; i += kT) {
-    const int b = t.rank * per + i;
+  for (int i = threadIdx.x; i < per + (t.rank == 0); i += kT) {
+    const int b = i < per ? t.rank * per + i : kSmBins;
     uint32_t c = 0;
     u64 e = 0;
 #pragma unroll
@@ -568,7 +586,7 @@ FLINT_DEV Cut resolve(Team<kT> &t, const RowPart<kHeld, kT> &r, const Dist &dist
     g.lo = ~t.all_max(~lo);
     while (g.n > (uint32_t)kSmList) {
       const int sh = g.shift(10);
-      for (int i = threadIdx.x; i < kSmBins; i += kT) s.cnt[i] = 0, s.eps[i] = 0;
+      for (int i = threadIdx.x; i <= kSmBins; i += kT) s.cnt[i] = 0, s.eps[i] = 0;
       __syncthreads();
       r.find(in,
              [&](float z, int i) {
@@ -837,7 +855,7 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
 
   // ---- the general row, and one with more equal logits than CTA 0 holds
   if (tid == 0) s.list_n = 0, s.mine_n = 0;
-  for (int i = tid; i < kSmBins; i += kT) s.cnt[i] = 0, s.eps[i] = 0;
+  for (int i = tid; i <= kSmBins; i += kT) s.cnt[i] = 0, s.eps[i] = 0;
   const float M = key_z((uint32_t)t.all_max(zkey(top)));
   if (M == -kInf) {
     if (t.rank == 0 && tid == 0) {
@@ -864,15 +882,14 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
         far_units += Dist::far_units(d);  // up to 2^13 each, 2^9 elements a thread
 
     });
-    long long far_c, far_u;
-    t.scan((long long)far_n, &far_c);
-    t.scan((long long)far_units, &far_u);
-    const int fp = t.post((u64)far_c, (u64)far_u);
+    far_n = __reduce_add_sync(0xffffffffu, far_n);
+    far_units = __reduce_add_sync(0xffffffffu, far_units);
+    if (lane == 0 && far_n) {
+      atomicAdd(&s.cnt[kSmBins], far_n);
+      atomicAdd(&s.eps[kSmBins], far_units);
+    }
     merge_bins(t, [](int b) { return b; });
-    Sum far{0, 0.0};
-    u64 fu = 0;
-    for (int i = 0; i < t.size; ++i) far.c += (uint32_t)s.slot[fp][i].a, fu += s.slot[fp][i].b;
-    far.m = Dist::mass(far.c, fu, kSmBins);
+    const Sum far{s.tcnt[kSmBins], s.tmass[kSmBins]};
     uint32_t bc[(kSmBins / kT)];
     double bm[(kSmBins / kT)];
     Sum all;
