@@ -25,8 +25,7 @@
 //      equal logits) are narrowed down by bins of the key in the cluster first;
 //   4. the kept mass in index order, p in units of 2^-44, by pieces of 128
 //      elements, and the token whose running mass passes u times the total.
-// All sums are of integers, or of doubles that are multiples of one power of
-// two and exact: a row's result is the same for every run, batch,
+// All sums are of integers: a row's result is the same for every run, batch,
 // cluster size and alignment.
 #include <algorithm>
 
@@ -51,15 +50,16 @@ constexpr float kFarUnit = 35184372088832.f;  // 2^45: 2^13 for the first behind
 constexpr uint32_t kNoneKey = 0x007fffffu;     // -inf: never chosen
 
 typedef unsigned long long u64;
+typedef long long i64;
 
 struct SampleShared {
   union {
     struct {
       // this CTA's bins and the cluster's; the last is all behind the bins
       uint32_t cnt[kSmBins + 2], eps[kSmBins + 2], tcnt[kSmBins + 2];
-      double tmass[kSmBins + 2];
+      i64 tmass[kSmBins + 2];
     };
-    long long chunk[kSmChunks];  // the last step's
+    i64 chunk[kSmChunks];  // the last step's
   };
   u64 list[kSmList];
   u64 sorted[kSmShort], mine[kSmShort];
@@ -70,14 +70,14 @@ struct SampleShared {
   } slot[2][kSmMaxCluster];
   uint32_t red_c[kSmMaxThreads / 32];
   u64 red_a[kSmMaxThreads / 32];
-  double red_b[kSmMaxThreads / 32];
+  i64 red_b[kSmMaxThreads / 32];
   u64 res_key[2];
-  double res_mass[2];
+  i64 res_mass[2];
   uint32_t list_n, mine_n;
   int found;
   uint32_t at_n, at_above;
-  double at_mass;
-  long long at_sum;
+  i64 at_mass;
+  i64 at_sum;
   float bin_lo, bin_hi;
 };
 
@@ -172,17 +172,6 @@ struct RowPart {
   }
 };
 
-// 2^(-i / 32), rounded
-__constant__ double kRoot[32] = {
-    0x1.0000000000000p+0, 0x1.f50765b6e4540p-1, 0x1.ea4afa2a490dap-1, 0x1.dfc97337b9b5fp-1,
-    0x1.d5818dcfba487p-1, 0x1.cb720dcef9069p-1, 0x1.c199bdd85529cp-1, 0x1.b7f76f2fb5e47p-1,
-    0x1.ae89f995ad3adp-1, 0x1.a5503b23e255dp-1, 0x1.9c49182a3f090p-1, 0x1.93737b0cdc5e5p-1,
-    0x1.8ace5422aa0dbp-1, 0x1.82589994cce13p-1, 0x1.7a11473eb0187p-1, 0x1.71f75e8ec5f74p-1,
-    0x1.6a09e667f3bcdp-1, 0x1.6247eb03a5585p-1, 0x1.5ab07dd485429p-1, 0x1.5342b569d4f82p-1,
-    0x1.4bfdad5362a27p-1, 0x1.44e086061892dp-1, 0x1.3dea64c123422p-1, 0x1.371a7373aa9cbp-1,
-    0x1.306fe0a31b715p-1, 0x1.29e9df51fdee1p-1, 0x1.2387a6e756238p-1, 0x1.1d4873168b9aap-1,
-    0x1.172b83c7d517bp-1, 0x1.11301d0125b51p-1, 0x1.0b5586cf9890fp-1, 0x1.059b0d3158574p-1};
-
 struct Dist {
   float M, c;
   // log2 of p(max) / p(z), >= 0; +inf where p = 0 (-inf)
@@ -217,27 +206,27 @@ struct Dist {
     hi += __float_as_uint(t);
     lo += __float_as_uint(fmaf(r, 17592186044416.f, 12582912.f));
   }
-  FLINT_DEV static long long whole(uint32_t hi, uint32_t lo, uint32_t n) {
-    return ((long long)(hi - n * 0x4B000000u) << 22) + (int)(lo - n * 0x4B400000u);
+  FLINT_DEV static i64 whole(uint32_t hi, uint32_t lo, uint32_t n) {
+    return ((i64)(hi - n * 0x4B000000u) << 22) + (int)(lo - n * 0x4B400000u);
   }
   FLINT_DEV uint32_t units_of(float z, int b) const {
     const float d = (*this)(z);
     return b == kSmBins ? far_units(d) : units(d, (float)b);
   }
-  // the mass that a count and such a sum stand for
-  FLINT_DEV static double mass(u64 n, u64 units, int b) {
-    if (b == kSmBins) return rounded((double)units / kFarUnit);
-    // 2^(-b / 32) = 2^-(b / 32) 2^-(b % 32 / 32)
-    const double first = __longlong_as_double(__double_as_longlong(kRoot[b & 31]) -
-                                              ((long long)(b >> 5) << 52));
-    return rounded(first * ((double)n - (double)units * (1.0 / kEpsUnit)));
+  // the mass that a count and such a sum stand for, in units of 2^-33 (of a
+  // row at most 2^51)
+  FLINT_DEV static i64 mass(u64 n, u64 units, int b) {
+    if (b == kSmBins) return fixed((double)units / kFarUnit);
+    const double first = ex2((float)b * (-1.f / kSmSteps));  // (to 2^-22: the same for all)
+    return fixed(first * ((double)n - (double)units * (1.0 / kEpsUnit)));
   }
-  // to a multiple of 2^-33: sums of these up to 2^19 are exact in any order
-  FLINT_DEV static double rounded(double x) {
-    const double kBig = 786432.0;  // 1.5 x 2^19
-    return (x + kBig) - kBig;
+  // x <= 2^18 to the nearest such unit: the low bits of its sum with 1.5 x 2^19
+  FLINT_DEV static i64 fixed(double x) {
+    return __double_as_longlong(x + 786432.0) - __double_as_longlong(786432.0);
   }
+  FLINT_DEV i64 mass_of(u64 key) const { return fixed(p(key_z((uint32_t)(key >> 32)))); }
 };
+
 FLINT_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 FLINT_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -251,7 +240,7 @@ FLINT_DEV T *cluster_at(T *p, int r) {
 
 struct Sum {
   uint32_t c;
-  double m;
+  i64 m;
 };
 
 template <int kT>
@@ -280,54 +269,52 @@ struct Team {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s->red_a[threadIdx.x >> 5] = a;
     __syncthreads();
+#pragma unroll
     for (int i = 0; i < kT / 32; ++i) a = a > s->red_a[i] ? a : s->red_a[i];
     return a;
   }
   // Sums before each thread's, of integers that fit 63 bits
-  FLINT_DEV long long scan(long long x, long long *total) {
+  FLINT_DEV i64 scan(i64 x, i64 *total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long inc = x;
+    i64 inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const i64 y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     __syncthreads();
     if (lane == 31) s->red_a[w] = (u64)inc;
     __syncthreads();
-    long long before = 0, all = 0;
+    i64 before = 0, all = 0;
     for (int i = 0; i < kT / 32; ++i) {
       if (i == w) before = all;
-      all += (long long)s->red_a[i];
+      all += (i64)s->red_a[i];
     }
     *total = all;
     return before + inc - x;
   }
   // Sums before each thread's (exclusive, in thread order); *total the block's
-  FLINT_DEV Sum scan(uint32_t c, double m, Sum *total) {
+  FLINT_DEV Sum scan(uint32_t c, i64 m, Sum *total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     uint32_t ic = c;
-    double im = m;
+    i64 im = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t c2 = __shfl_up_sync(0xffffffffu, ic, o);
-      const double m2 = __shfl_up_sync(0xffffffffu, im, o);
+      const i64 m2 = __shfl_up_sync(0xffffffffu, im, o);
       if (lane >= o) ic += c2, im += m2;
     }
     __syncthreads();
     if (lane == 31) s->red_c[w] = ic, s->red_b[w] = im;
     __syncthreads();
-    Sum before{0, 0.0}, all{0, 0.0};
+    Sum before{0, 0}, all{0, 0};
+#pragma unroll
     for (int i = 0; i < kT / 32; ++i) {
       if (i == w) before = all;
       all.c += s->red_c[i], all.m += s->red_b[i];
     }
     *total = all;
-    // lane 0's is the warps' sum exactly; the others' own value is taken out
-    // by the shuffle, not by a subtraction
-    const uint32_t pc = __shfl_up_sync(0xffffffffu, ic, 1);
-    const double pm = __shfl_up_sync(0xffffffffu, im, 1);
-    return lane ? Sum{before.c + pc, before.m + pm} : before;
+    return {before.c + ic - c, before.m + im - m};
   }
   // the CTAs' values to every CTA's slots, there after the next sync; returns
   // the set they are in
@@ -354,24 +341,24 @@ struct Team {
 struct Goal {
   bool count;
   uint32_t want;
-  double mass;
-  FLINT_DEV bool reached(uint32_t c, double m) const { return count ? c >= want : m >= mass; }
+  i64 mass;
+  FLINT_DEV bool reached(uint32_t c, i64 m) const { return count ? c >= want : m >= mass; }
 };
 struct Cut {
   u64 key;      // the last kept element
-  double mass;  // mass down to it
+  i64 mass;  // mass down to it
 };
 // Elements of the order between two keys, and what lies before them
 struct Range {
   u64 lo, hi;
   uint32_t n, above;
-  double mass_above;
+  i64 mass_above;
   FLINT_DEV int shift(int bits) const {
     const int top = 64 - __clzll((long long)(hi - lo));
     return top > bits ? top - bits : 0;
   }
   // to bin b of those that `shift` makes
-  FLINT_DEV void narrow(int b, int sh, uint32_t n_, uint32_t above_, double mass_) {
+  FLINT_DEV void narrow(int b, int sh, uint32_t n_, uint32_t above_, i64 mass_) {
     hi -= (u64)b << sh;
     const u64 width = ((u64)1 << sh) - 1;
     if (hi - lo > width) lo = hi - width;
@@ -383,8 +370,8 @@ struct Range {
 // thread (before: the sums in front of the thread's bins); every thread gets
 // it with its sums, -1 if the bins do not reach the goal.
 template <int kPer, int kT>
-FLINT_DEV int pick(Team<kT> &t, const Goal &g, const uint32_t (&c)[kPer], const double (&m)[kPer],
-                   const Sum &before, uint32_t *n, uint32_t *above, double *mass) {
+FLINT_DEV int pick(Team<kT> &t, const Goal &g, const uint32_t (&c)[kPer], const i64 (&m)[kPer],
+                   const Sum &before, uint32_t *n, uint32_t *above, i64 *mass) {
   SampleShared &s = *t.s;
   __syncthreads();
   if (threadIdx.x == 0) s.found = 0x7fffffff;
@@ -452,16 +439,16 @@ FLINT_DEV Cut resolve_list(Team<kT> &t, const Dist &dist, int b, int m, Range r,
     }
     __syncthreads();
     const uint32_t c[1] = {tid < kSmSub ? s.scnt[tid] : 0u};
-    const double ms[1] = {c[0] ? Dist::mass(c[0], s.seps[tid], b) : 0.0};
+    const i64 ms[1] = {c[0] ? Dist::mass(c[0], s.seps[tid], b) : 0};
     Sum total;
     Sum before = t.scan(c[0], ms[0], &total);
     before.c += r.above, before.m += r.mass_above;
     uint32_t n, above;
-    double mass;
+    i64 mass;
     int x = pick<1>(t, goal, c, ms, before, &n, &above, &mass);
     if (x < 0) {
       // the bins' masses round short of the goal: the last element
-      x = pick<1>(t, Goal{true, r.above + total.c, 0.0}, c, ms, before, &n, &above, &mass);
+      x = pick<1>(t, Goal{true, r.above + total.c, 0}, c, ms, before, &n, &above, &mass);
     }
     r.narrow(x, sh, n, above, mass);
   }
@@ -486,16 +473,16 @@ FLINT_DEV Cut resolve_list(Team<kT> &t, const Dist &dist, int b, int m, Range r,
   __syncthreads();
   const u64 k = tid < n ? s.sorted[tid] : 0;
   const uint32_t c[1] = {tid < n ? 1u : 0u};
-  const double p[1] = {tid < n ? Dist::rounded(dist.p(key_z((uint32_t)(k >> 32)))) : 0.0};
+  const i64 p[1] = {tid < n ? dist.mass_of(k) : 0};
   Sum total;
   Sum before = t.scan(c[0], p[0], &total);
   before.c += r.above, before.m += r.mass_above;
   uint32_t x_n, x_above;
-  double x_mass;
+  i64 x_mass;
   int x = pick<1>(t, goal, c, p, before, &x_n, &x_above, &x_mass);
-  if (x < 0) x = pick<1>(t, Goal{true, r.above + total.c, 0.0}, c, p, before, &x_n, &x_above, &x_mass);
+  if (x < 0) x = pick<1>(t, Goal{true, r.above + total.c, 0}, c, p, before, &x_n, &x_above, &x_mass);
   const u64 key = n ? s.sorted[x] : 0;
-  return {key, n ? x_mass + Dist::rounded(dist.p(key_z((uint32_t)(key >> 32)))) : r.mass_above};
+  return {key, n ? x_mass + dist.mass_of(key) : r.mass_above};
 }
 
 // The logits of bin b, as an interval: two comparisons an element where the
@@ -509,9 +496,16 @@ template <int kT>
 FLINT_DEV InBin in_bin(Team<kT> &t, const Dist &dist, int b) {
   SampleShared &s = *t.s;
   if (threadIdx.x < 32) {
-    // the first key nearer than `bound` (M's at the latest)
+    // the first key nearer than `bound` (M's at the latest): near the guess
+    // M - bound / c, else by a search
     auto nearer = [&](float bound) {
       uint32_t a = kNoneKey + 1, e = zkey(dist.M);
+      const uint32_t g = zkey(dist.M - __fdividef(bound, dist.c));
+      if (g > a + 16 && g < e && e - g > 16) {
+        const uint32_t k = g - 16 + threadIdx.x;
+        const uint32_t yes = __ballot_sync(0xffffffffu, dist(key_z(k)) < bound);
+        if (yes && !(yes & 1u)) return g - 16 + __ffs(yes) - 1;
+      }
       while (a < e) {
         const uint32_t step = (e - a) / 32 + 1;
         const u64 k = a + (u64)step * threadIdx.x;
@@ -545,7 +539,7 @@ FLINT_DEV void merge_bins(Team<kT> &t, F bin_of) {
 #pragma unroll
     for (int q = 0; q < kSmMaxCluster; ++q)
       if (q < t.size) c += t.of(s.cnt, q)[b], e += t.of(s.eps, q)[b];
-    const double mass = c ? Dist::mass(c, e, bin_of(b)) : 0.0;
+    const i64 mass = c ? Dist::mass(c, e, bin_of(b)) : 0;
 #pragma unroll
     for (int q = 0; q < kSmMaxCluster; ++q)
       if (q < t.size) t.of(s.tcnt, q)[b] = c, t.of(s.tmass, q)[b] = mass;
@@ -555,12 +549,12 @@ FLINT_DEV void merge_bins(Team<kT> &t, F bin_of) {
 
 // A thread's merged bins and the sums in front of them
 template <int kT>
-FLINT_DEV Sum scan_bins(Team<kT> &t, uint32_t (&c)[(kSmBins / kT)], double (&m)[(kSmBins / kT)], Sum *total) {
+FLINT_DEV Sum scan_bins(Team<kT> &t, uint32_t (&c)[kSmBins / kT], i64 (&m)[kSmBins / kT], Sum *total) {
   uint32_t cs = 0;
-  double ms = 0;
+  i64 ms = 0;
 #pragma unroll
-  for (int i = 0; i < (kSmBins / kT); ++i) {
-    c[i] = t.s->tcnt[(kSmBins / kT) * threadIdx.x + i], m[i] = t.s->tmass[(kSmBins / kT) * threadIdx.x + i];
+  for (int i = 0; i < kSmBins / kT; ++i) {
+    c[i] = t.s->tcnt[kSmBins / kT * threadIdx.x + i], m[i] = t.s->tmass[kSmBins / kT * threadIdx.x + i];
     cs += c[i], ms += m[i];
   }
   return t.scan(cs, ms, total);
@@ -571,7 +565,7 @@ FLINT_DEV Sum scan_bins(Team<kT> &t, uint32_t (&c)[(kSmBins / kT)], double (&m)[
 // the same answer.
 template <bool kHeld, int kT>
 FLINT_DEV Cut resolve(Team<kT> &t, const RowPart<kHeld, kT> &r, const Dist &dist, int b, uint32_t n,
-                      uint32_t above, double mass_above, const Goal &goal) {
+                      uint32_t above, i64 mass_above, const Goal &goal) {
   SampleShared &s = *t.s;
   Range g{0, ~0ull, n, above, mass_above};
   const InBin in = in_bin(t, dist, b);
@@ -598,16 +592,16 @@ FLINT_DEV Cut resolve(Team<kT> &t, const RowPart<kHeld, kT> &r, const Dist &dist
                }
              });
       merge_bins(t, [&](int) { return b; });
-      uint32_t c[(kSmBins / kT)];
-      double ms[(kSmBins / kT)];
+      uint32_t c[kSmBins / kT];
+      i64 ms[kSmBins / kT];
       Sum total;
       Sum before = scan_bins(t, c, ms, &total);
       before.c += g.above, before.m += g.mass_above;
       uint32_t x_n, x_above;
-      double x_mass;
+      i64 x_mass;
       int x = pick<kSmBins / kT>(t, goal, c, ms, before, &x_n, &x_above, &x_mass);
       if (x < 0)
-        x = pick<kSmBins / kT>(t, Goal{true, g.above + total.c, 0.0}, c, ms, before, &x_n, &x_above,
+        x = pick<kSmBins / kT>(t, Goal{true, g.above + total.c, 0}, c, ms, before, &x_n, &x_above,
                          &x_mass);
       g.narrow(x, sh, x_n, x_above, x_mass);
     }
@@ -654,7 +648,7 @@ FLINT_DEV float min_p_logit(float M, const Settings &p) {
   return fminf(__double2float_ru((double)M + (double)p.T * log((double)p.min_p)), M);
 }
 FLINT_DEV void write_token(const SampleArgs &a, int row, int token, float z, float M, float T,
-                           long long total) {
+                           i64 total) {
   a.token[row] = token;
   if (a.logprob) {
     const double y = z == M ? 0.0 : ((double)z - (double)M) / (double)T;
@@ -696,8 +690,8 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
   if (m > kSmShort) {
     lo = ~t.block_max(~lo);
     // (the masses are not looked at: any bin serves)
-    from = resolve_list(t, dist, 0, m, Range{lo, hi, (uint32_t)m, 0, 0.0},
-                        Goal{true, (uint32_t)min(k, m), 0.0}).key;
+    from = resolve_list(t, dist, 0, m, Range{lo, hi, (uint32_t)m, 0, 0},
+                        Goal{true, (uint32_t)min(k, m), 0}).key;
     __syncthreads();
   }
   if (tid == 0) s.mine_n = 0;
@@ -720,9 +714,9 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
   const float z = key_z((uint32_t)(x >> 32));
   const float pz = tid < K ? dist.p(z) : 0.f;
   Sum total;
-  Sum before = t.scan(0, Dist::rounded(pz), &total);
+  Sum before = t.scan(0, Dist::fixed(pz), &total);
   bool kept = pz > 0.f;
-  if (p.top_p < 1.f) kept &= before.m < (double)p.top_p * total.m;
+  if (p.top_p < 1.f) kept &= (double)before.m < (double)p.top_p * (double)total.m;
   if (p.min_p > 0.f) kept &= z >= min_p_logit(M, p);
   if (tid == 0) kept = true;  // the first one always
   // in index order
@@ -739,13 +733,13 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
   }
   __syncthreads();
   x = tid < nk ? s.sorted[s.scnt[tid]] : 0;
-  long long units = 0, sum;
+  i64 units = 0, sum;
   if (tid < nk) {
     uint32_t uh = 0, ul = 0;
     Dist::add_units(dist.p(key_z((uint32_t)(x >> 32))), uh, ul);
     units = Dist::whole(uh, ul, 1);
   }
-  const long long at = t.scan(units, &sum);
+  const i64 at = t.scan(units, &sum);
   const double goal = p.u * (double)sum;
   // the first whose running mass passes the goal, or the last (u = 1)
   if (tid == 0) s.found = nk - 1;
@@ -890,28 +884,28 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     }
     merge_bins(t, [](int b) { return b; });
     const Sum far{s.tcnt[kSmBins], s.tmass[kSmBins]};
-    uint32_t bc[(kSmBins / kT)];
-    double bm[(kSmBins / kT)];
+    uint32_t bc[kSmBins / kT];
+    i64 bm[kSmBins / kT];
     Sum all;
     const Sum before = scan_bins(t, bc, bm, &all);
 
     // the bin a goal falls in, and the cut in it
     auto search = [&](const Goal &g) {
       uint32_t n, above;
-      double mass;
+      i64 mass;
       const int b = pick<kSmBins / kT>(t, g, bc, bm, before, &n, &above, &mass);
       if (b >= 0) return resolve(t, r, dist, b, n, above, mass, g);
       if (!far.c) return Cut{0ull, all.m};  // nothing behind the bins: no cut
       return resolve(t, r, dist, kSmBins, far.c, all.c, all.m, g);
     };
-    double mass = all.m + far.m;
+    i64 mass = all.m + far.m;
     if (use_k && (uint32_t)kk < all.c + far.c) {
-      const Cut c = search(Goal{true, (uint32_t)kk, 0.0});
+      const Cut c = search(Goal{true, (uint32_t)kk, 0});
       cut = c.key;
       mass = c.mass;
     }
     if (use_p) {
-      const Cut c = search(Goal{false, 0, (double)set.top_p * mass});
+      const Cut c = search(Goal{false, 0, (i64)ceil((double)set.top_p * (double)mass)});
       if (c.key > cut) cut = c.key;
     }
   }
@@ -966,13 +960,13 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
   // a thread has `per` pieces next to each other
   const int per = (chunks + kT - 1) / kT;
   const int c_lo = min(chunks, tid * per), c_hi = min(chunks, c_lo + per);
-  long long w = 0, mine;
+  i64 w = 0, mine;
   for (int c = c_lo; c < c_hi; ++c) w += s.chunk[c];
-  const long long at = t.scan(w, &mine);
+  const i64 at = t.scan(w, &mine);
   const int q = t.post((u64)mine, 0);
   t.sync();
-  long long total = 0;
-  for (int i = 0; i < t.size; ++i) total += (long long)s.slot[q][i].a;
+  i64 total = 0;
+  for (int i = 0; i < t.size; ++i) total += (i64)s.slot[q][i].a;
   if (set.u >= 1.0) {
     // the last kept token, however small its share
     u64 last = 0;
@@ -988,16 +982,16 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
   // the CTA, then the piece, then the element whose running mass passes the
   // goal (u < 1: one does)
   int cta = 0;
-  long long start = 0;
+  i64 start = 0;
   for (; cta < t.size - 1; ++cta) {
-    const long long x = (long long)s.slot[q][cta].a;
+    const i64 x = (i64)s.slot[q][cta].a;
     if ((double)(start + x) > goal) break;
     start += x;
   }
   if (cta != t.rank) return;  // (nobody reads another CTA's memory any more)
   if (tid == 0) s.found = chunks - 1;
   __syncthreads();
-  long long x = start + at;
+  i64 x = start + at;
   for (int c = c_lo; c < c_hi; ++c) {
     x += s.chunk[c];
     if ((double)x > goal) {
@@ -1020,7 +1014,7 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     const float4 v = r.load(i);
     z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
   }
-  long long own[4], sum = 0;
+  i64 own[4], sum = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t uh = 0, ul = 0;
@@ -1028,10 +1022,10 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     own[j] = Dist::whole(uh, ul, 1);
     sum += own[j];
   }
-  long long inc = sum;
+  i64 inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    const i64 y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   x = s.at_sum + inc - sum;
