@@ -485,7 +485,7 @@ typedef struct {
  *           tokens with the same slot, which one's 16-byte pieces a row ends
  *           up with is not defined
  *   pos     int32 [T], >= 0
- *   rope_dim 0, or a multiple of 16 up to head_dim; theta > 0, finite
+ *   rope_dim 0, or a multiple of 16 up to head_dim; 1 <= theta <= 1e300
  *   q_norm, k_norm  bf16 [head_dim] or NULL
  *   q_out   bf16, token t's row at q_out + t * q_out_stride; may be q itself
  *           (same stride), and may not overlap it otherwise
@@ -525,7 +525,8 @@ FLINT_API int flint_kv_append(const flint_kv_cache *cache, const uint16_t *q, in
  *           the prefix's neither (out = 0).  lens[b] above max_pages *
  *           page_size records FLINT_EDEVICE and is cut to that
  *   prefix_pages  int32 [ceil(prefix_len / page_size)] (NULL with prefix_len
- *           = 0); prefix_len >= 0.  prefix_len + max_pages * page_size <= 2^30
+ *           = 0); prefix_len >= 0.  prefix_len + max_pages * page_size <= 2^30, and
+ *           B times that <= 2^36
  *   window  0: none
  *   sinks   fp32 [q_heads] or NULL;  lse fp32 [B][q_heads] or NULL
  *   ws      workspace of flint_attn_workspace_bytes(B, q_heads, heads,

@@ -36,13 +36,13 @@ EXPORTS = ("flint_version", "flint_strerror", "flint_last_cuda_error", "flint_wo
            "flint_debug_prefill_stage_ms")
 
 
-
 class flint_kv_cache(C.Structure):
     """One layer's pages (make_kv_cache)."""
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("type", C.c_int), ("num_pages", C.c_int),
                 ("page_size", C.c_int), ("heads", C.c_int), ("head_dim", C.c_int),
                 ("page_stride", C.c_int64), ("head_stride", C.c_int64),
                 ("token_stride", C.c_int64), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+    _device = None  # of its tensors; None: raw addresses
 
 
 _lib = None
@@ -321,11 +321,16 @@ def flint_int4_gemv_noalloc_status(stream=None) -> int:
 
 
 # ------------------------------------------------- the cache, its attention, sampling
-def _local(where: str, *tensors):
-    """The tensors' addresses.  Refuses tensors that are not on the current
-    CUDA device: the call launches there, and ``stream`` is one of its
-    streams."""
+def _local(where: str, *tensors, cache=None):
+    """The tensors' addresses.  Refuses tensors (the cache's among them) that
+    are not on the current CUDA device: the call launches there, and
+    ``stream`` is one of its streams."""
     dev, ptrs = None, []
+    if cache is not None and cache._device is not None:
+        import torch
+        dev = cache._device
+        if dev != torch.cuda.current_device():
+            raise FlintError(FLINT_EINVAL, where)
     for t in tensors:
         if t is None or isinstance(t, int):
             ptrs.append(t)
@@ -360,6 +365,7 @@ def make_kv_cache(k, v, k_scale=None, v_scale=None) -> flint_kv_cache:
                            FLINT_KV_E4M3, pages, page, heads, dim, k.stride(0), k.stride(1),
                            k.stride(2), _ptr(k_scale), _ptr(v_scale))
     cache._tensors = (k, v, k_scale, v_scale)
+    cache._device = k.get_device()
     return cache
 
 
@@ -373,7 +379,7 @@ def flint_kv_append(cache: flint_kv_cache, q, q_stride: int, k, k_stride: int, v
                     stream=None):
     """``cache``: from ``make_kv_cache``."""
     q, k, v, slots, pos, q_norm, k_norm, q_out, ws = _local(
-        "flint_kv_append", q, k, v, slots, pos, q_norm, k_norm, q_out, ws)
+        "flint_kv_append", q, k, v, slots, pos, q_norm, k_norm, q_out, ws, cache=cache)
     _check(lib().flint_kv_append(C.byref(cache), q, q_stride, k, k_stride, v, v_stride, T, q_heads,
                                  slots, pos, rope_dim, 1 if interleaved else 0, theta, q_norm,
                                  k_norm, q_out, q_out_stride, ws, ws_bytes, _stream(stream)),
@@ -386,7 +392,7 @@ def flint_attn_decode(cache: flint_kv_cache, q, q_stride: int, B: int, q_heads: 
                       stream=None):
     """``cache``: from ``make_kv_cache``."""
     q, page_table, lens, prefix_pages, sinks, out, lse, ws = _local(
-        "flint_attn_decode", q, page_table, lens, prefix_pages, sinks, out, lse, ws)
+        "flint_attn_decode", q, page_table, lens, prefix_pages, sinks, out, lse, ws, cache=cache)
     _check(lib().flint_attn_decode(C.byref(cache), q, q_stride, B, q_heads, page_table, max_pages,
                                    lens, prefix_pages, prefix_len, scale, window, sinks, out,
                                    out_stride, lse, ws, ws_bytes, _stream(stream)),

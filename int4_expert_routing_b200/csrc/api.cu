@@ -323,7 +323,7 @@ int flint_kv_append(const flint_kv_cache *cache, const uint16_t *q, int64_t q_st
   const int64_t d = cache->head_dim, n = cache->heads * d;
   if (!rows_ok(k, k_stride, n) || !rows_ok(v, v_stride, n) || !slots || !pos ||
       (reinterpret_cast<uintptr_t>(slots) & 7u) || !aligned4(pos) || rope_dim < 0 ||
-      rope_dim % 16 || rope_dim > d || !(theta > 0.0) || theta > 1e300 ||
+      rope_dim % 16 || rope_dim > d || !(theta >= 1.0) || theta > 1e300 ||
       (q_norm && !aligned16(q_norm)) || (k_norm && !aligned16(k_norm)) || !aligned16(ws) ||
       ws_bytes < flint_workspace_bytes(FLINT_OP_APPEND, T))
     return FLINT_EINVAL;
@@ -354,6 +354,8 @@ int flint_attn_decode(const flint_kv_cache *cache, const uint16_t *q, int64_t q_
       (out == q && out_stride != q_stride) || !aligned4(page_table) || max_pages < 1 ||
       !aligned4(lens) || prefix_len < 0 || (prefix_len > 0 && !aligned4(prefix_pages)) ||
       (int64_t)max_pages * cache->page_size + prefix_len > ((int64_t)1 << 30) ||
+      // the running tiles of all sequences are 32-bit
+      ((int64_t)max_pages * cache->page_size + prefix_len) * B > ((int64_t)1 << 36) ||
       !(scale == scale) || window < 0 || (sinks && !aligned4(sinks)) || (lse && !aligned4(lse)) ||
       !aligned16(ws) ||
       ws_bytes < flint_attn_workspace_bytes(B, q_heads, cache->heads, cache->head_dim))

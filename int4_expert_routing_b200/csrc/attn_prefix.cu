@@ -464,6 +464,9 @@ __global__ void __launch_bounds__(PreCfg<kD, kF8>::kThreads, 1)
         }
       }
       if (!active) continue;
+      // (at least the smallest normal number: times 0 a masked product's -inf
+      // would be NaN; a seen one times 2^-126 is 0 beside any other)
+      fac = fmaxf(fac, 1.17549435e-38f);
       fence_async();
       tc_fence_before();
       __syncwarp();

@@ -139,3 +139,23 @@ def test_struct_matches_the_header():
     names = re.findall(r"(\w+)\s*;", body)
     assert names == [n for n, _ in F.flint_kv_cache._fields_]
     assert ctypes.sizeof(F.flint_kv_cache) == 80
+
+
+def test_theta_below_one_and_tables_too_large():
+    """Angles that grow with the pair's number, and more tiles in all than the plan counts."""
+    refused(append, theta=0.5)
+    refused(attend, B=F.MAX_ATTN_B, max_pages=1 << 20, prefix_len=20)
+
+
+def test_binding_refuses_a_cache_of_another_device():
+    """The cache's tensors are on device 1, the call's (raw addresses) wherever the current one is."""
+    torch = pytest.importorskip("torch")
+    c = cache()
+    c._device = 1
+    current = torch.cuda.current_device
+    torch.cuda.current_device = lambda: 0
+    try:
+        refused(append, c)
+        refused(attend, c)
+    finally:
+        torch.cuda.current_device = current

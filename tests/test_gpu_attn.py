@@ -210,6 +210,15 @@ def test_large_and_small_scores():
             assert ((lse[b] - wl).abs() <= 2.0 ** -20 * (wl.abs() + 500)).all()
 
 
+@pytest.mark.parametrize("kv,dim,B", [("bf16", 128, 20), ("e4m3", 64, 40), ("bf16", 64, 1)])
+def test_shared_prefix_scales(kv, dim, B):
+    """Scale 0 (all keys alike), a negative and a tiny one, the prefix ending inside a tile."""
+    s = build(33 + dim, [(7 * b) % 40 for b in range(B)], 16, 2, dim, kv, 32, 300, False)
+    for scale in (0.0, -0.1, 1e-30):
+        out, lse, _ = call(to_dev(s), scale)
+        check(s, out, lse, scale, rows=range(0, B, 4))
+
+
 def test_nan_and_inf_where_they_are_seen():
     """A NaN key or value shows in its own sequence and KV head, and in no other."""
     s = build(41, [100, 100, 100], 8, 2, 64, "bf16", 16, 0, False)
