@@ -23,11 +23,12 @@
 //      elements are gathered into one CTA, which narrows them down by 512 bins
 //      of the key and orders the last few.  More than fit there (flat rows,
 //      equal logits) are narrowed down by bins of the key in the cluster first;
-//   4. the kept mass in index order, p in units of 2^-44, by pieces of 128
-//      elements, and the token whose running mass passes u times the total.
+//   4. the kept mass in index order, p in units of 2^-44, by pieces of 256 or
+//      512 elements, and the token whose running mass passes u times the total.
 // All sums are of integers: a row's result is the same for every run, batch,
 // cluster size and alignment.
 #include <algorithm>
+#include <cstddef>
 
 #include "common.cuh"
 #include "internal.h"
@@ -42,8 +43,7 @@ constexpr int kSmSubBits = 9, kSmSub = 1 << kSmSubBits;  // bins of a list's key
 constexpr int kSmOrder = 128;       // elements put in order at once
 constexpr int kSmShort = 256;       // largest k of the short path
 constexpr int kSmMaxCluster = 8;
-constexpr int kSmChunk = 128;       // elements of a sum of the last step
-constexpr int kSmChunks = FLINT_MAX_VOCAB / kSmChunk + 2;
+constexpr int kSmPieces = FLINT_MAX_VOCAB / 512 + 8;  // sums of the last step in a CTA
 constexpr int kSmHold = 160 * 1024;  // bytes of a row that a CTA holds at most
 constexpr float kEpsUnit = 524288.f;          // 2^19
 constexpr float kFarUnit = 35184372088832.f;  // 2^45: 2^13 for the first behind the bins
@@ -59,7 +59,7 @@ struct SampleShared {
       uint32_t cnt[kSmBins + 2], eps[kSmBins + 2], tcnt[kSmBins + 2];
       i64 tmass[kSmBins + 2];
     };
-    i64 chunk[kSmChunks];  // the last step's
+    i64 piece[kSmPieces];  // the last step's
   };
   u64 list[kSmList];
   u64 sorted[kSmShort], mine[kSmShort];
@@ -121,6 +121,7 @@ struct RowPart {
     return v;
   }
   static constexpr int kAhead = kHeld ? 2 : 4;
+  static constexpr int kPiece = 128 * kAhead;  // elements of a sum of the last step
   // f(logit, row index) for this thread's elements
   template <typename F>
   FLINT_DEV void each(F f) const {
@@ -188,26 +189,64 @@ struct Dist {
   // What an element of a bin adds to the bin's integer: its shortfall
   // e = 1 - 2^(edge/32 - d) from the bin's first value, by the series of the
   // exponential (y < 0.0217: off by less than y^4/24 = 2^-26), or behind the
-  // bins its value itself.
+  // bins its value itself; each as the bits of its sum with 2^23 (kUnitsBase
+  // an element goes out when a bin is read).
+  static constexpr uint32_t kUnitsBase = 0x4B000000u;
   FLINT_DEV static uint32_t units(float d, float edge) {
     const float y = fmaxf(fmaf(edge, -1.f / kSmSteps, d), 0.f) * 0.69314718f;
     const float e = y * fmaf(y, fmaf(y, 1.f / 6, -0.5f), 1.f);
-    return __float_as_uint(fmaf(e, kEpsUnit, 8388608.f)) & 0x7fffffu;
+    return __float_as_uint(fmaf(e, kEpsUnit, 8388608.f));
   }
   FLINT_DEV static uint32_t far_units(float d) {
-    return __float_as_uint(fmaf(ex2(-d), kFarUnit, 8388608.f)) & 0x7fffffu;
+    return __float_as_uint(fmaf(ex2(-d), kFarUnit, 8388608.f));
   }
-  // p <= 1 in units of 2^-44, as hi 2^22 + lo, added to the sums of both: hi
-  // is p to the nearest 2^-22 (adding 2^23 leaves it in the low bits), lo what
-  // that rounded off.  The constants in the bits go out at the end (whole).
-  FLINT_DEV static void add_units(float p, uint32_t &hi, uint32_t &lo) {
-    const float t = fmaf(p, 4194304.f, 8388608.f);
-    const float r = fmaf(t - 8388608.f, -1.f / 4194304.f, p);
-    hi += __float_as_uint(t);
-    lo += __float_as_uint(fmaf(r, 17592186044416.f, 12582912.f));
+  // Two p <= 1 in units of 2^-44, as hi 2^22 + lo, added to the sums of both:
+  // hi is p to the nearest 2^-22 (adding 2 leaves it in the low bits), lo what
+  // that rounded off (adding 1.5 x 2^-21, likewise).  The constants in the bits
+  // go out at the end (whole, of n numbers).
+  FLINT_DEV static void add_units(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+    const uint64_t p = pair2(p0, p1), t = add2(p, pair2(2.f, 2.f));
+    const uint64_t r = fma2(add2(t, pair2(-2.f, -2.f)), pair2(-1.f, -1.f), p);
+    const uint64_t q = add2(r, pair2(kLoBase, kLoBase));
+    hi = hi + (uint32_t)t + (uint32_t)(t >> 32);
+    lo = lo + (uint32_t)q + (uint32_t)(q >> 32);
   }
+  static constexpr float kLoBase = 7.152557373046875e-7f;  // 1.5 x 2^-21, 0x35400000
   FLINT_DEV static i64 whole(uint32_t hi, uint32_t lo, uint32_t n) {
-    return ((i64)(hi - n * 0x4B000000u) << 22) + (int)(lo - n * 0x4B400000u);
+    return ((i64)(hi - n * 0x40000000u) << 22) + (int)(lo - n * 0x35400000u);
+  }
+  FLINT_DEV static i64 units44(float p) {
+    uint32_t hi = 0, lo = 0;
+    add_units(p, 0.f, hi, lo);
+    return whole(hi, lo, 2);
+  }
+  // Two elements of the first pass over the bins, in pairs: d, and for those
+  // with d < 32 their count and units to the bins at `at` (the address of
+  // bin 0 less 4 kUnitsBase; the units kEpsAt bytes behind).
+  template <int kEpsAt>
+  FLINT_DEV static void bin2(uint64_t z, uint64_t minus_m, uint64_t minus_c, uint32_t at, float &d0,
+                             float &d1) {
+    const uint64_t d = mul2(add2(z, minus_m), minus_c);
+    uint64_t t;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;"
+        : "=l"(t)
+        : "l"(d), "l"(pair2(kSmSteps, kSmSteps)), "l"(pair2(8388608.f, 8388608.f)));
+    const uint64_t edge = add2(t, pair2(-8388608.f, -8388608.f));
+    const uint64_t y = mul2(fma2(edge, pair2(-1.f / kSmSteps, -1.f / kSmSteps), d),
+                            pair2(0.69314718f, 0.69314718f));
+    const uint64_t e =
+        mul2(y, fma2(y, fma2(y, pair2(1.f / 6, 1.f / 6), pair2(-0.5f, -0.5f)), pair2(1.f, 1.f)));
+    const uint64_t u = fma2(e, pair2(kEpsUnit, kEpsUnit), pair2(8388608.f, 8388608.f));
+    unpair2(d, d0, d1);
+    auto add = [&](float dd, uint32_t tt, uint32_t uu) {
+      asm volatile(
+          "{\n.reg .pred p;\nsetp.lt.f32 p, %0, 0f42000000;\n@p red.shared.add.u32 [%1], 1;\n"
+          "@p red.shared.add.u32 [%1 + %3], %2;\n}\n" ::"f"(dd),
+          "r"(at + (tt << 2)), "r"(uu), "n"(kEpsAt)
+          : "memory");
+    };
+    add(d0, (uint32_t)t, (uint32_t)u);
+    add(d1, (uint32_t)(t >> 32), (uint32_t)(u >> 32));
   }
   FLINT_DEV uint32_t units_of(float z, int b) const {
     const float d = (*this)(z);
@@ -439,7 +478,7 @@ FLINT_DEV Cut resolve_list(Team<kT> &t, const Dist &dist, int b, int m, Range r,
     }
     __syncthreads();
     const uint32_t c[1] = {tid < kSmSub ? s.scnt[tid] : 0u};
-    const i64 ms[1] = {c[0] ? Dist::mass(c[0], s.seps[tid], b) : 0};
+    const i64 ms[1] = {c[0] ? Dist::mass(c[0], s.seps[tid] - c[0] * Dist::kUnitsBase, b) : 0};
     Sum total;
     Sum before = t.scan(c[0], ms[0], &total);
     before.c += r.above, before.m += r.mass_above;
@@ -538,7 +577,10 @@ FLINT_DEV void merge_bins(Team<kT> &t, F bin_of) {
     u64 e = 0;
 #pragma unroll
     for (int q = 0; q < kSmMaxCluster; ++q)
-      if (q < t.size) c += t.of(s.cnt, q)[b], e += t.of(s.eps, q)[b];
+      if (q < t.size) {
+        const uint32_t n = t.of(s.cnt, q)[b];
+        c += n, e += t.of(s.eps, q)[b] - n * Dist::kUnitsBase;
+      }
     const i64 mass = c ? Dist::mass(c, e, bin_of(b)) : 0;
 #pragma unroll
     for (int q = 0; q < kSmMaxCluster; ++q)
@@ -734,11 +776,7 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
   __syncthreads();
   x = tid < nk ? s.sorted[s.scnt[tid]] : 0;
   i64 units = 0, sum;
-  if (tid < nk) {
-    uint32_t uh = 0, ul = 0;
-    Dist::add_units(dist.p(key_z((uint32_t)(x >> 32))), uh, ul);
-    units = Dist::whole(uh, ul, 1);
-  }
+  if (tid < nk) units = Dist::units44(dist.p(key_z((uint32_t)(x >> 32))));
   const i64 at = t.scan(units, &sum);
   const double goal = p.u * (double)sum;
   // the first whose running mass passes the goal, or the last (u = 1)
@@ -863,19 +901,55 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
   u64 cut = 0;  // kept: (z, index) at or before this in the order
   if (use_k || use_p) {
     uint32_t far_n = 0, far_units = 0;
-    r.each([&](float z, int) {
-      const float d = dist(z);
-      if (d < (float)kSmBins / kSmSteps) {
-        float edge;
-        const int b = Dist::bin(d, &edge);
-        atomicAdd(&s.cnt[b], 1u);
-        atomicAdd(&s.eps[b], Dist::units(d, edge));
+    auto far = [&](float z, float d) {
+      if ((d >= (float)kSmBins / kSmSteps) & (z > -kInf))
+        ++far_n, far_units += Dist::far_units(d);  // up to 2^13 each, 2^9 elements a thread
+    };
+    if (M < kInf && dist.c < kInf) {
+      // (z - M) c has no infinity less or times another: (M - z) c without tests
+      const uint64_t minus_m = pair2(-M, -M), minus_c = pair2(-dist.c, -dist.c);
+      const uint32_t at = smem_addr(s.cnt) - 4 * Dist::kUnitsBase;
+      constexpr int kEpsAt = (int)(offsetof(SampleShared, eps) - offsetof(SampleShared, cnt));
+      constexpr int kAhead = RowPart<kHeld, kT>::kAhead;
+      for (int i0 = tid; i0 < r.n4; i0 += kAhead * kT) {
+        float4 v[kAhead];
+        float most = 0.f;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int i = i0 + u * kT;
+          v[u] = i < r.n4 ? r.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          float d[4];
+          Dist::bin2<kEpsAt>(pair2(v[u].x, v[u].y), minus_m, minus_c, at, d[0], d[1]);
+          Dist::bin2<kEpsAt>(pair2(v[u].z, v[u].w), minus_m, minus_c, at, d[2], d[3]);
+          most = fmaxf(fmaxf(most, fmaxf(d[0], d[1])), fmaxf(d[2], d[3]));
+        }
+        if (most >= (float)kSmBins / kSmSteps) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            far(v[u].x, dist(v[u].x)), far(v[u].y, dist(v[u].y));
+            far(v[u].z, dist(v[u].z)), far(v[u].w, dist(v[u].w));
+          }
+        }
       }
-      far_n += (d >= (float)kSmBins / kSmSteps) & (z > -kInf);
-      if ((d >= (float)kSmBins / kSmSteps) & (d < 46.f))
-        far_units += Dist::far_units(d);  // up to 2^13 each, 2^9 elements a thread
-
-    });
+    } else {
+      // infinities: one by one
+#pragma unroll 1
+      for (int i = tid; i < 4 * r.n4; i += kT) {
+        const int e = r.index0 + i;
+        const float z = e >= lo && e < hi ? reinterpret_cast<const float *>(r.z)[i] : -kInf;
+        const float d = dist(z);
+        if (d < (float)kSmBins / kSmSteps) {
+          float edge;
+          const int b = Dist::bin(d, &edge);
+          atomicAdd(&s.cnt[b], 1u);
+          atomicAdd(&s.eps[b], Dist::units(d, edge));
+        }
+        far(z, d);
+      }
+    }
     far_n = __reduce_add_sync(0xffffffffu, far_n);
     far_units = __reduce_add_sync(0xffffffffu, far_units);
     if (lane == 0 && far_n) {
@@ -883,7 +957,7 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
       atomicAdd(&s.eps[kSmBins], far_units);
     }
     merge_bins(t, [](int b) { return b; });
-    const Sum far{s.tcnt[kSmBins], s.tmass[kSmBins]};
+    const Sum behind{s.tcnt[kSmBins], s.tmass[kSmBins]};
     uint32_t bc[kSmBins / kT];
     i64 bm[kSmBins / kT];
     Sum all;
@@ -895,11 +969,11 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
       i64 mass;
       const int b = pick<kSmBins / kT>(t, g, bc, bm, before, &n, &above, &mass);
       if (b >= 0) return resolve(t, r, dist, b, n, above, mass, g);
-      if (!far.c) return Cut{0ull, all.m};  // nothing behind the bins: no cut
-      return resolve(t, r, dist, kSmBins, far.c, all.c, all.m, g);
+      if (!behind.c) return Cut{0ull, all.m};  // nothing behind the bins: no cut
+      return resolve(t, r, dist, kSmBins, behind.c, all.c, all.m, g);
     };
-    i64 mass = all.m + far.m;
-    if (use_k && (uint32_t)kk < all.c + far.c) {
+    i64 mass = all.m + behind.m;
+    if (use_k && (uint32_t)kk < all.c + behind.c) {
       const Cut c = search(Goal{true, (uint32_t)kk, 0});
       cut = c.key;
       mass = c.mass;
@@ -926,7 +1000,7 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     if (c > cut) cut = c;
   }
 
-  // kept mass: pieces of kSmChunk elements, one float4 a lane
+  // kept mass, by pieces of kPiece elements, kAhead float4 a lane
   const float zc = cut ? key_z((uint32_t)(cut >> 32)) : -kInf;
   const uint32_t ic = cut ? 0xffffffffu - (uint32_t)cut : 0x7fffffffu;
   auto p_of = [&](float z, int i) {
@@ -934,34 +1008,50 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     const bool kept = (z > zc) | ((z == zc) & ((uint32_t)i <= ic));
     return ex2(kept ? -dist(z) : -kInf);  // (no branch)
   };
-  const int chunks = (r.n4 + 31) / 32;  // at most kSmChunks
-  constexpr int kAhead = RowPart<kHeld, kT>::kAhead;
-  for (int c0 = warp; c0 < chunks; c0 += kAhead * (kT / 32)) {
+  constexpr int kAhead = RowPart<kHeld, kT>::kAhead, kPiece = RowPart<kHeld, kT>::kPiece;
+  const int pieces = (4 * r.n4 + kPiece - 1) / kPiece;  // at most kSmPieces
+  const uint64_t minus_m = pair2(-M, -M), cc = pair2(dist.c, dist.c);
+  for (int c = warp; c < pieces; c += kT / 32) {
     float4 v[kAhead];
+    bool tie = false;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int i = 32 * (c0 + j * (kT / 32)) + lane;
+      const int i = 32 * (kAhead * c + j) + lane;
       v[j] = i < r.n4 ? r.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
+      tie |= (v[j].x == zc) | (v[j].y == zc) | (v[j].z == zc) | (v[j].w == zc);
     }
+    if (__any_sync(0xffffffffu, tie)) {
+      // equals of the cut behind its index
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int c = c0 + j * (kT / 32), e = r.index0 + 4 * (32 * c + lane);
-      uint32_t uh = 0, ul = 0;
-      Dist::add_units(p_of(v[j].x, e), uh, ul);
-      Dist::add_units(p_of(v[j].y, e + 1), uh, ul);
-      Dist::add_units(p_of(v[j].z, e + 2), uh, ul);
-      Dist::add_units(p_of(v[j].w, e + 3), uh, ul);
-      uh = __reduce_add_sync(0xffffffffu, uh);
-      ul = __reduce_add_sync(0xffffffffu, ul);
-      if (lane == 0 && c < chunks) s.chunk[c] = Dist::whole(uh, ul, kSmChunk);
+      for (int j = 0; j < kAhead; ++j) {
+        const uint32_t e = (uint32_t)(r.index0 + 4 * (32 * (kAhead * c + j) + lane));
+        if (v[j].x == zc && e > ic) v[j].x = -kInf;
+        if (v[j].y == zc && e + 1 > ic) v[j].y = -kInf;
+        if (v[j].z == zc && e + 2 > ic) v[j].z = -kInf;
+        if (v[j].w == zc && e + 3 > ic) v[j].w = -kInf;
+      }
     }
+    uint32_t uh = 0, ul = 0;
+    // dist() in pairs: NaN (M and z both infinite) is 0 there too
+    auto two = [&](float a, float b) {
+      float x, y;
+      unpair2(mul2(add2(pair2(a, b), minus_m), cc), x, y);
+      x = ex2(a >= zc ? fminf(x, 0.f) : -kInf);
+      y = ex2(b >= zc ? fminf(y, 0.f) : -kInf);
+      Dist::add_units(x, y, uh, ul);
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) two(v[j].x, v[j].y), two(v[j].z, v[j].w);
+    uh = __reduce_add_sync(0xffffffffu, uh);
+    ul = __reduce_add_sync(0xffffffffu, ul);
+    if (lane == 0) s.piece[c] = Dist::whole(uh, ul, kPiece);
   }
   __syncthreads();
   // a thread has `per` pieces next to each other
-  const int per = (chunks + kT - 1) / kT;
-  const int c_lo = min(chunks, tid * per), c_hi = min(chunks, c_lo + per);
+  const int per = (pieces + kT - 1) / kT;
+  const int c_lo = min(pieces, tid * per), c_hi = min(pieces, c_lo + per);
   i64 w = 0, mine;
-  for (int c = c_lo; c < c_hi; ++c) w += s.chunk[c];
+  for (int c = c_lo; c < c_hi; ++c) w += s.piece[c];
   const i64 at = t.scan(w, &mine);
   const int q = t.post((u64)mine, 0);
   t.sync();
@@ -989,11 +1079,11 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     start += x;
   }
   if (cta != t.rank) return;  // (nobody reads another CTA's memory any more)
-  if (tid == 0) s.found = chunks - 1;
+  if (tid == 0) s.found = pieces - 1;
   __syncthreads();
   i64 x = start + at;
   for (int c = c_lo; c < c_hi; ++c) {
-    x += s.chunk[c];
+    x += s.piece[c];
     if ((double)x > goal) {
       atomicMin(&s.found, c);
       break;
@@ -1003,42 +1093,45 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
   const int c = s.found;
   if (c >= c_lo && c < c_hi) {
     x = start + at;
-    for (int i = c_lo; i < c; ++i) x += s.chunk[i];
+    for (int i = c_lo; i < c; ++i) x += s.piece[i];
     s.at_sum = x;
   }
   __syncthreads();
   if (warp) return;
-  const int i = 32 * c + lane, e = r.index0 + 4 * i;
-  float z[4] = {-kInf, -kInf, -kInf, -kInf};
-  if (i < r.n4) {
-    const float4 v = r.load(i);
-    z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
-  }
-  i64 own[4], sum = 0;
+  x = s.at_sum;
+#pragma unroll 1
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = 32 * (kAhead * c + k) + lane, e = r.index0 + 4 * i;
+    float z[4] = {-kInf, -kInf, -kInf, -kInf};
+    if (i < r.n4) {
+      const float4 v = r.load(i);
+      z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
+    }
+    i64 own[4], sum = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t uh = 0, ul = 0;
-    Dist::add_units(p_of(z[j], e + j), uh, ul);
-    own[j] = Dist::whole(uh, ul, 1);
-    sum += own[j];
-  }
-  i64 inc = sum;
+    for (int j = 0; j < 4; ++j) sum += own[j] = Dist::units44(p_of(z[j], e + j));
+    i64 inc = sum;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const i64 y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  x = s.at_sum + inc - sum;
-  int hit = -1;  // of this lane's four
+    for (int o = 1; o < 32; o <<= 1) {
+      const i64 y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    i64 run = x + inc - sum;
+    int hit = -1;  // of this lane's four
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x += own[j];
-    if (hit < 0 && (double)x > goal) hit = j;
+    for (int j = 0; j < 4; ++j) {
+      run += own[j];
+      if (hit < 0 && (double)run > goal) hit = j;
+    }
+    const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0);
+    if (hits) {
+      if (lane == __ffs(hits) - 1)
+        write_token(a, row, e + hit, hit == 0 ? z[0] : hit == 1 ? z[1] : hit == 2 ? z[2] : z[3], M,
+                    set.T, total);
+      return;
+    }
+    x = __shfl_sync(0xffffffffu, run, 31);
   }
-  const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0);
-  if (hits && lane == __ffs(hits) - 1)
-    write_token(a, row, e + hit, hit == 0 ? z[0] : hit == 1 ? z[1] : hit == 2 ? z[2] : z[3], M,
-                set.T, total);
 }
 
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st) {
