@@ -604,10 +604,11 @@ FLINT_DEV Sum scan_bins(Team<kT> &t, uint32_t (&c)[kSmBins / kT], i64 (&m)[kSmBi
 
 // The cut inside bin `b`, which holds n elements behind `above` earlier ones
 // with mass `mass_above`.  Every thread of the cluster takes part and gets
-// the same answer.
-template <bool kHeld, int kT>
+// the same answer.  gather(in) may hand over the bin's elements (InBin in) of
+// all the row itself, if they fit the list, and say so.
+template <bool kHeld, int kT, typename F>
 FLINT_DEV Cut resolve(Team<kT> &t, const RowPart<kHeld, kT> &r, const Dist &dist, int b, uint32_t n,
-                      uint32_t above, i64 mass_above, const Goal &goal) {
+                      uint32_t above, i64 mass_above, const Goal &goal, F gather) {
   SampleShared &s = *t.s;
   Range g{0, ~0ull, n, above, mass_above};
   const InBin in = in_bin(t, dist, b);
@@ -649,11 +650,12 @@ FLINT_DEV Cut resolve(Team<kT> &t, const RowPart<kHeld, kT> &r, const Dist &dist
     }
   }
   // gather into CTA 0, which has the rest to do
-  r.find(in,
-         [&](float z, int i) {
-           const u64 k = order_key(z, i);
-           if (k >= g.lo && k <= g.hi) collect(t, k);
-         });
+  if (n > (uint32_t)kSmList || !gather(in))
+    r.find(in,
+           [&](float z, int i) {
+             const u64 k = order_key(z, i);
+             if (k >= g.lo && k <= g.hi) collect(t, k);
+           });
   hand_over(t);
   t.sync();
   const int at = t.resolved & 1;  // (a slow CTA may still read the other)
@@ -898,7 +900,41 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
   }
   const Dist dist{M, __fdiv_rn(1.4426950408889634f, greedy ? 1.f : set.T)};
   const bool use_k = few || (k > 0 && k < a.V), use_p = !few && set.top_p < 1.f;
-  u64 cut = 0;  // kept: (z, index) at or before this in the order
+  const float zmin = !few && set.min_p > 0.f ? min_p_logit(M, set) : -kInf;
+  u64 cut = 0;      // kept: (z, index) at or before this in the order
+  int summed = -1;  // with the search for the cut: the elements of its bin, in the list
+
+  // The mass of the elements at or above `from`, by pieces of kPiece elements,
+  // kAhead float4 a lane; first(v, e0) sees them before (e0: the row index of
+  // v[0].x, the next 128 on).
+  constexpr int kAhead = RowPart<kHeld, kT>::kAhead, kPiece = RowPart<kHeld, kT>::kPiece;
+  const int pieces = (4 * r.n4 + kPiece - 1) / kPiece;  // at most kSmPieces
+  auto sum_pieces = [&](float from, auto first) {
+    const uint64_t minus_m = pair2(-M, -M), cc = pair2(dist.c, dist.c);
+    for (int c = warp; c < pieces; c += kT / 32) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = 32 * (kAhead * c + j) + lane;
+        v[j] = i < r.n4 ? r.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
+      }
+      first(v, r.index0 + 4 * (32 * kAhead * c + lane));
+      uint32_t uh = 0, ul = 0;
+      // dist() in pairs: NaN (M and z both infinite) is 0 there too
+      auto two = [&](float a, float b) {
+        float x, y;
+        unpair2(mul2(add2(pair2(a, b), minus_m), cc), x, y);
+        x = ex2(a >= from ? fminf(x, 0.f) : -kInf);
+        y = ex2(b >= from ? fminf(y, 0.f) : -kInf);
+        Dist::add_units(x, y, uh, ul);
+      };
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) two(v[j].x, v[j].y), two(v[j].z, v[j].w);
+      uh = __reduce_add_sync(0xffffffffu, uh);
+      ul = __reduce_add_sync(0xffffffffu, ul);
+      if (lane == 0) s.piece[c] = Dist::whole(uh, ul, kPiece);
+    }
+  };
   if (use_k || use_p) {
     uint32_t far_n = 0, far_units = 0;
     auto far = [&](float z, float d) {
@@ -910,7 +946,6 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
       const uint64_t minus_m = pair2(-M, -M), minus_c = pair2(-dist.c, -dist.c);
       const uint32_t at = smem_addr(s.cnt) - 4 * Dist::kUnitsBase;
       constexpr int kEpsAt = (int)(offsetof(SampleShared, eps) - offsetof(SampleShared, cnt));
-      constexpr int kAhead = RowPart<kHeld, kT>::kAhead;
       for (int i0 = tid; i0 < r.n4; i0 += kAhead * kT) {
         float4 v[kAhead];
         float most = 0.f;
@@ -963,14 +998,41 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     Sum all;
     const Sum before = scan_bins(t, bc, bm, &all);
 
+    // Where the row is read again from L2 (and the list is this CTA's), the
+    // only cut's bin is gathered in the pass that sums what lies before it:
+    // 128 rows of 150,144: @@ us instead of @@.
+    auto gather = [&](const InBin &in, uint32_t n) {
+      if (kHeld || t.size > 1 || few || use_k == use_p || in.hi == kInf) return false;
+      sum_pieces(fmaxf(key_z(zkey(in.hi) + 1), zmin), [&](float4(&v)[kAhead], int e0) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          hits |= in(v[j].x) ? 1u << (4 * j) : 0u;
+          hits |= in(v[j].y) ? 2u << (4 * j) : 0u;
+          hits |= in(v[j].z) ? 4u << (4 * j) : 0u;
+          hits |= in(v[j].w) ? 8u << (4 * j) : 0u;
+        }
+#pragma unroll 1
+        for (; hits; hits &= hits - 1) {
+          const int j = __ffs(hits) - 1, e = e0 + 128 * (j >> 2) + (j & 3);
+          collect(t, order_key(reinterpret_cast<const float *>(r.z)[e - r.index0], e));
+        }
+      });
+      summed = (int)n;
+      return true;
+    };
     // the bin a goal falls in, and the cut in it
     auto search = [&](const Goal &g) {
       uint32_t n, above;
       i64 mass;
       const int b = pick<kSmBins / kT>(t, g, bc, bm, before, &n, &above, &mass);
-      if (b >= 0) return resolve(t, r, dist, b, n, above, mass, g);
+      if (b >= 0) return resolve(t, r, dist, b, n, above, mass, g, [&](const InBin &in) {
+        return gather(in, n);
+      });
       if (!behind.c) return Cut{0ull, all.m};  // nothing behind the bins: no cut
-      return resolve(t, r, dist, kSmBins, behind.c, all.c, all.m, g);
+      return resolve(t, r, dist, kSmBins, behind.c, all.c, all.m, g, [&](const InBin &in) {
+        return gather(in, behind.c);
+      });
     };
     i64 mass = all.m + behind.m;
     if (use_k && (uint32_t)kk < all.c + behind.c) {
@@ -996,11 +1058,10 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     return;
   }
   if (set.min_p > 0.f) {
-    const u64 c = (u64)zkey(min_p_logit(M, set)) << 32;
+    const u64 c = (u64)zkey(zmin) << 32;
     if (c > cut) cut = c;
   }
 
-  // kept mass, by pieces of kPiece elements, kAhead float4 a lane
   const float zc = cut ? key_z((uint32_t)(cut >> 32)) : -kInf;
   const uint32_t ic = cut ? 0xffffffffu - (uint32_t)cut : 0x7fffffffu;
   auto p_of = [&](float z, int i) {
@@ -1008,43 +1069,31 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
     const bool kept = (z > zc) | ((z == zc) & ((uint32_t)i <= ic));
     return ex2(kept ? -dist(z) : -kInf);  // (no branch)
   };
-  constexpr int kAhead = RowPart<kHeld, kT>::kAhead, kPiece = RowPart<kHeld, kT>::kPiece;
-  const int pieces = (4 * r.n4 + kPiece - 1) / kPiece;  // at most kSmPieces
-  const uint64_t minus_m = pair2(-M, -M), cc = pair2(dist.c, dist.c);
-  for (int c = warp; c < pieces; c += kT / 32) {
-    float4 v[kAhead];
-    bool tie = false;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = 32 * (kAhead * c + j) + lane;
-      v[j] = i < r.n4 ? r.load(i) : make_float4(-kInf, -kInf, -kInf, -kInf);
-      tie |= (v[j].x == zc) | (v[j].y == zc) | (v[j].z == zc) | (v[j].w == zc);
+  if (summed >= 0) {
+    // what is kept of the cut's bin
+    for (int i = tid; i < summed; i += kT) {
+      const u64 x = s.list[i];
+      if (x >= cut)
+        atomicAdd(reinterpret_cast<u64 *>(&s.piece[(key_index(x) - r.index0) / kPiece]),
+                  (u64)Dist::units44(dist.p(key_z((uint32_t)(x >> 32)))));
     }
-    if (__any_sync(0xffffffffu, tie)) {
+  } else {
+    sum_pieces(zc, [&](float4(&v)[kAhead], int e0) {
+      bool tie = false;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        tie |= (v[j].x == zc) | (v[j].y == zc) | (v[j].z == zc) | (v[j].w == zc);
+      if (!__any_sync(0xffffffffu, tie)) return;
       // equals of the cut behind its index
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const uint32_t e = (uint32_t)(r.index0 + 4 * (32 * (kAhead * c + j) + lane));
+        const uint32_t e = (uint32_t)(e0 + 128 * j);
         if (v[j].x == zc && e > ic) v[j].x = -kInf;
         if (v[j].y == zc && e + 1 > ic) v[j].y = -kInf;
         if (v[j].z == zc && e + 2 > ic) v[j].z = -kInf;
         if (v[j].w == zc && e + 3 > ic) v[j].w = -kInf;
       }
-    }
-    uint32_t uh = 0, ul = 0;
-    // dist() in pairs: NaN (M and z both infinite) is 0 there too
-    auto two = [&](float a, float b) {
-      float x, y;
-      unpair2(mul2(add2(pair2(a, b), minus_m), cc), x, y);
-      x = ex2(a >= zc ? fminf(x, 0.f) : -kInf);
-      y = ex2(b >= zc ? fminf(y, 0.f) : -kInf);
-      Dist::add_units(x, y, uh, ul);
-    };
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) two(v[j].x, v[j].y), two(v[j].z, v[j].w);
-    uh = __reduce_add_sync(0xffffffffu, uh);
-    ul = __reduce_add_sync(0xffffffffu, ul);
-    if (lane == 0) s.piece[c] = Dist::whole(uh, ul, kPiece);
+    });
   }
   __syncthreads();
   // a thread has `per` pieces next to each other

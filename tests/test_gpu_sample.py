@@ -190,6 +190,45 @@ def test_sample_strides_batches_and_repeats(V, stride):
     assert none is None and torch.equal(t3, token.cpu())
 
 
+@pytest.mark.parametrize("k,p,m", [(0, 0.9, 0.0), (0, 0.999, 1e-4), (400, 1.0, 0.0), (900, 0.8, 0.01),
+                                   (30, 0.9, 0.0), (0, 1.0, 0.05)])
+@pytest.mark.parametrize("T", [0.2, 1.0])
+def test_sample_large_batch_equals_single_rows(k, p, m, T):
+    """Rows that a full batch reads again from L2 give the bits that they give alone: heavy and
+    flat tails, equal logits, masked ones, infinities, more than a list of a bin's elements."""
+    g = gen(k + int(1000 * p))
+    B, V, stride = 70, 50001, 50003
+    z = torch.empty(B, stride).exponential_(generator=g) * 1.1
+    z[1] = 0.25
+    z[2] = torch.floor(4 * z[2])
+    z[3, ::3] = -math.inf
+    z[4, 7:9], z[5, 40000] = math.inf, math.inf
+    z[6, ::5] = math.nan
+    z[7] *= 1e-3
+    z[8] *= 1e3
+    z[9, :] = -math.inf
+    z[10, :25000] = z[10, 0]
+    u = torch.rand(B, generator=g)
+    u[11], u[12] = 0.0, 1.0
+    par = [full(B, T), full(B, k, torch.int32), full(B, p), full(B, m), u]
+    token, lp = call_strided(z, V, par)
+    for b in list(range(16)) + [69]:
+        one, l1 = call(z[b:b + 1, :V].contiguous(), *[x[b:b + 1] for x in par])
+        assert int(one[0]) == int(token[b]), b
+        assert torch.equal(l1[0], lp[b]), b
+    rows = [0, 1, 2, 3, 7, 13, 69]
+    check(z[rows, :V].contiguous(), *[x[rows] for x in par])
+
+
+def call_strided(z, V, par):
+    z, dev = z.cuda(), [x.cuda() for x in par]
+    token = torch.full((z.shape[0],), -7, dtype=torch.int32, device="cuda")
+    lp = torch.full((z.shape[0],), 7.0, device="cuda")
+    F.flint_sample(z, z.shape[1], z.shape[0], V, *dev, token, lp)
+    torch.cuda.synchronize()
+    return token.cpu(), lp.cpu()
+
+
 def test_sample_distribution():
     """20,000 rows of one small distribution: each token as often as it should be, within six
     standard deviations."""
