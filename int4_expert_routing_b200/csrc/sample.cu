@@ -282,9 +282,9 @@ struct Sum {
   i64 m;
 };
 
-template <int kT>
+// kT threads: the block (kBar 0), or its first ones, on a barrier of their own
+template <int kT, int kBar = 0>
 struct Team {
-
   SampleShared *s;
   int rank, size, parity = 0, resolved = 0;
   FLINT_DEV void sync() {
@@ -299,20 +299,30 @@ struct Team {
   FLINT_DEV T *of(T *p, int r) {
     return cluster_at(p, r);
   }
-  // The block's largest a, to every thread
-  FLINT_DEV u64 block_max(u64 a) {
+  FLINT_DEV static void block_sync() {
+    if (kBar == 0) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kT) : "memory");
+  }
+  // largest of the warp's
+  FLINT_DEV static u64 warp_max(u64 a) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(a >> 32));
     const uint32_t lo =
         __reduce_max_sync(0xffffffffu, (uint32_t)(a >> 32) == hi ? (uint32_t)a : 0u);
-    a = ((u64)hi << 32) | lo;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s->red_a[threadIdx.x >> 5] = a;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kT / 32; ++i) a = a > s->red_a[i] ? a : s->red_a[i];
-    return a;
+    return ((u64)hi << 32) | lo;
   }
-  // Sums before each thread's, of integers that fit 63 bits
+  // The block's largest a, to every thread.  (Here and in the scans each warp
+  // joins the warps' results by shuffles; a loop over them in every warp took
+  // 1,000 to 3,000 cycles.)
+  FLINT_DEV u64 block_max(u64 a) {
+    const int lane = threadIdx.x & 31;
+    a = warp_max(a);
+    block_sync();
+    if (lane == 0) s->red_a[threadIdx.x >> 5] = a;
+    block_sync();
+    return warp_max(lane < kT / 32 ? s->red_a[lane] : 0);
+  }
+  // Sums before each thread's (exclusive, in thread order), of integers that
+  // fit 63 bits; *total the block's
   FLINT_DEV i64 scan(i64 x, i64 *total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     i64 inc = x;
@@ -321,18 +331,19 @@ struct Team {
       const i64 y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    __syncthreads();
-    if (lane == 31) s->red_a[w] = (u64)inc;
-    __syncthreads();
-    i64 before = 0, all = 0;
-    for (int i = 0; i < kT / 32; ++i) {
-      if (i == w) before = all;
-      all += (i64)s->red_a[i];
+    block_sync();
+    if (lane == 31) s->red_b[w] = inc;
+    block_sync();
+    const i64 own = lane < kT / 32 ? s->red_b[lane] : 0;
+    i64 all = own;
+#pragma unroll
+    for (int o = 1; o < kT / 32; o <<= 1) {
+      const i64 y = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += y;
     }
-    *total = all;
-    return before + inc - x;
+    *total = __shfl_sync(0xffffffffu, all, kT / 32 - 1);
+    return __shfl_sync(0xffffffffu, all - own, w) + inc - x;
   }
-  // Sums before each thread's (exclusive, in thread order); *total the block's
   FLINT_DEV Sum scan(uint32_t c, i64 m, Sum *total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     uint32_t ic = c;
@@ -343,17 +354,23 @@ struct Team {
       const i64 m2 = __shfl_up_sync(0xffffffffu, im, o);
       if (lane >= o) ic += c2, im += m2;
     }
-    __syncthreads();
+    block_sync();
     if (lane == 31) s->red_c[w] = ic, s->red_b[w] = im;
-    __syncthreads();
-    Sum before{0, 0}, all{0, 0};
+    block_sync();
+    const uint32_t own_c = lane < kT / 32 ? s->red_c[lane] : 0;
+    const i64 own_m = lane < kT / 32 ? s->red_b[lane] : 0;
+    uint32_t all_c = own_c;
+    i64 all_m = own_m;
 #pragma unroll
-    for (int i = 0; i < kT / 32; ++i) {
-      if (i == w) before = all;
-      all.c += s->red_c[i], all.m += s->red_b[i];
+    for (int o = 1; o < kT / 32; o <<= 1) {
+      const uint32_t c2 = __shfl_up_sync(0xffffffffu, all_c, o);
+      const i64 m2 = __shfl_up_sync(0xffffffffu, all_m, o);
+      if (lane >= o) all_c += c2, all_m += m2;
     }
-    *total = all;
-    return {before.c + ic - c, before.m + im - m};
+    total->c = __shfl_sync(0xffffffffu, all_c, kT / 32 - 1);
+    total->m = __shfl_sync(0xffffffffu, all_m, kT / 32 - 1);
+    return {__shfl_sync(0xffffffffu, all_c - own_c, w) + ic - c,
+            __shfl_sync(0xffffffffu, all_m - own_m, w) + im - m};
   }
   // the CTAs' values to every CTA's slots, there after the next sync; returns
   // the set they are in
@@ -701,27 +718,18 @@ FLINT_DEV void write_token(const SampleArgs &a, int row, int token, float z, flo
 }
 
 // The rest of a short row, in the one CTA whose list holds its m candidates,
-// the first k of the order among them.
-template <int kT>
-FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, int k, bool greedy,
-                            const Settings &p) {
-  SampleShared &s = *t.s;
+// the first k of the order among them; those from `from` on are at most
+// kSmShort.  By kSmShort threads: a barrier and a scan of the whole block take
+// two to four times as long.
+FLINT_DEV void finish_few(SampleShared &s, const SampleArgs &a, int row, int m, int k, u64 from,
+                          bool greedy, const Settings &p) {
+  Team<kSmShort, 1> t;
+  t.s = &s;
   const int tid = threadIdx.x;
-  const float kInf = __int_as_float(0x7f800000);
-  if (m == 0) {
-    if (tid == 0) {
-      a.token[row] = -1;
-      if (a.logprob) a.logprob[row] = -kInf;
-    }
-    return;
-  }
-  u64 hi = 0, lo = ~0ull;
-  for (int i = tid; i < m; i += kT) {
-    const u64 x = s.list[i];
-    lo = x < lo ? x : lo, hi = x > hi ? x : hi;
-  }
+  u64 hi = 0;
+  for (int i = tid; i < m; i += kSmShort) hi = max(hi, s.list[i]);
+  if (tid == 0) s.mine_n = 0;
   hi = t.block_max(hi);
-  const float M = key_z((uint32_t)(hi >> 32));
   if (greedy) {
     if (tid == 0) {
       a.token[row] = key_index(hi);
@@ -729,22 +737,13 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
     }
     return;
   }
+  const float M = key_z((uint32_t)(hi >> 32));
   const Dist dist{M, __fdiv_rn(1.4426950408889634f, p.T)};
-  u64 from = 0;
-  if (m > kSmShort) {
-    lo = ~t.block_max(~lo);
-    // (the masses are not looked at: any bin serves)
-    from = resolve_list(t, dist, 0, m, Range{lo, hi, (uint32_t)m, 0, 0},
-                        Goal{true, (uint32_t)min(k, m), 0}).key;
-    __syncthreads();
-  }
-  if (tid == 0) s.mine_n = 0;
-  __syncthreads();
-  for (int i = tid; i < m; i += kT) {
+  for (int i = tid; i < m; i += kSmShort) {
     const u64 x = s.list[i];
     if (x >= from) s.mine[atomicAdd(&s.mine_n, 1u)] = x;  // at most kSmShort
   }
-  __syncthreads();
+  t.block_sync();
   const int n = (int)s.mine_n;
   if (tid < n) {
     const u64 x = s.mine[tid];
@@ -752,7 +751,7 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
     for (int j = 0; j < n; ++j) before += s.mine[j] > x;
     s.sorted[before] = x;
   }
-  __syncthreads();
+  t.block_sync();
   const int K = min(k, n);
   u64 x = tid < K ? s.sorted[tid] : 0;
   const float z = key_z((uint32_t)(x >> 32));
@@ -765,17 +764,17 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
   if (tid == 0) kept = true;  // the first one always
   // in index order
   if (tid == 0) s.mine_n = 0;
-  __syncthreads();
+  t.block_sync();
   const u64 by_index = ((u64)(uint32_t)key_index(x) << 32) | (uint32_t)tid;
   if (kept) s.mine[atomicAdd(&s.mine_n, 1u)] = by_index;
-  __syncthreads();
+  t.block_sync();
   const int nk = (int)s.mine_n;
   if (kept) {
     int at = 0;
     for (int j = 0; j < nk; ++j) at += s.mine[j] < by_index;
     s.scnt[at] = (uint32_t)tid;  // place in the order
   }
-  __syncthreads();
+  t.block_sync();
   x = tid < nk ? s.sorted[s.scnt[tid]] : 0;
   i64 units = 0, sum;
   if (tid < nk) units = Dist::units44(dist.p(key_z((uint32_t)(x >> 32))));
@@ -783,10 +782,39 @@ FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, in
   const double goal = p.u * (double)sum;
   // the first whose running mass passes the goal, or the last (u = 1)
   if (tid == 0) s.found = nk - 1;
-  __syncthreads();
+  t.block_sync();
   if (tid < nk && (double)(at + units) > goal) atomicMin(&s.found, tid);
-  __syncthreads();
+  t.block_sync();
   if (tid == s.found) write_token(a, row, key_index(x), key_z((uint32_t)(x >> 32)), M, p.T, sum);
+}
+
+template <int kT>
+FLINT_DEV void finish_short(Team<kT> &t, const SampleArgs &a, int row, int m, int k, bool greedy,
+                            const Settings &p) {
+  SampleShared &s = *t.s;
+  if (m == 0) {
+    if (threadIdx.x == 0) {
+      a.token[row] = -1;
+      if (a.logprob) a.logprob[row] = -__int_as_float(0x7f800000);
+    }
+    return;
+  }
+  u64 from = 0;
+  if (m > kSmShort && !greedy) {
+    u64 hi = 0, lo = ~0ull;
+    for (int i = threadIdx.x; i < m; i += kT) {
+      const u64 x = s.list[i];
+      lo = min(lo, x), hi = max(hi, x);
+    }
+    hi = t.block_max(hi);
+    lo = ~t.block_max(~lo);
+    // (the masses are not looked at: any bin serves)
+    const Dist dist{key_z((uint32_t)(hi >> 32)), __fdiv_rn(1.4426950408889634f, p.T)};
+    from = resolve_list(t, dist, 0, m, Range{lo, hi, (uint32_t)m, 0, 0},
+                        Goal{true, (uint32_t)min(k, m), 0}).key;
+    __syncthreads();
+  }
+  if (threadIdx.x < kSmShort) finish_few(s, a, row, m, k, from, greedy, p);
 }
 
 template <bool kHeld, int kT>
@@ -851,30 +879,46 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
 
   // ---- few kept tokens
   if (few) {
-    // the largest threshold found that at least kk threads' maxima reach
+    // the largest threshold found that at least kk threads' maxima reach, and
+    // with a cluster one that its share of kk reach in every CTA
     const uint32_t mine = zkey(top);
     uint32_t a0 = __reduce_min_sync(0xffffffffu, mine), a1 = __reduce_max_sync(0xffffffffu, mine);
     if (lane == 0) s.red_a[warp] = ((u64)a1 << 32) | a0;
     __syncthreads();
-    for (int i = 0; i < kT / 32; ++i) {
-      a0 = min(a0, (uint32_t)s.red_a[i]);
-      a1 = max(a1, (uint32_t)(s.red_a[i] >> 32));
+    {
+      const u64 x = s.red_a[lane % (kT / 32)];
+      a0 = __reduce_min_sync(0xffffffffu, (uint32_t)x);
+      a1 = __reduce_max_sync(0xffffffffu, (uint32_t)(x >> 32));
     }
-    // all reach a0; fewer than kk reach a1 + 1
+    // all reach a0; too few reach `end`
     uint32_t count = kT;
-    u64 end = (u64)a1 + 1;
-    while (end - a0 > 1 && count > (uint32_t)kk + kk / 4 + 2) {
-      const uint32_t mid = a0 + (uint32_t)((end - a0) / 2);
-      const uint32_t c = (uint32_t)__syncthreads_count(mine >= mid);
-      if (c >= (uint32_t)kk) a0 = mid, count = c;
-      else end = mid;
+    auto raise = [&](uint32_t want) {
+      u64 end = (u64)a1 + 1;
+      while (end - a0 > 1 && count > want + want / 4 + 2) {
+        const uint32_t mid = a0 + (uint32_t)((end - a0) / 2);
+        const uint32_t c = (uint32_t)__syncthreads_count(mine >= mid);
+        if (c >= want) a0 = mid, count = c;
+        else end = mid;
+      }
+    };
+    raise((uint32_t)kk);
+    uint32_t from = a0;
+    if (t.size > 1) {
+      // (a CTA far below the others brings the second one down: the first holds)
+      raise((uint32_t)(kk + t.size - 1) / t.size);
+      cluster_wait();
+      const int q = t.post(a0, 0);
+      t.sync();
+      for (int i = 0; i < t.size; ++i) a0 = min(a0, (uint32_t)s.slot[q][i].a);
+      from = max(from, a0);
+    } else {
+      cluster_wait();
     }
-    const uint32_t from = max(a0, kNoneKey + 1);
+    from = max(from, kNoneKey + 1);
     const float zfrom = key_z(from);
     if (mine >= from)
       r.find([&](float z) { return z >= zfrom; },
              [&](float z, int i) { collect(t, order_key(z, i)); });
-    cluster_wait();
     hand_over(t);
     t.sync();
     const uint32_t m = *t.of(&s.list_n, 0);
@@ -885,7 +929,7 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
       return;
     }
   }
-  cluster_wait();
+  cluster_wait();  // the first one's, or what the few tokens' path arrived at
 
   // ---- the general row, and one with more equal logits than CTA 0 holds
   if (tid == 0) s.list_n = 0, s.mine_n = 0;
@@ -1000,7 +1044,7 @@ __global__ void __launch_bounds__(kT, 1) k_sample(const __grid_constant__ Sample
 
     // Where the row is read again from L2 (and the list is this CTA's), the
     // only cut's bin is gathered in the pass that sums what lies before it:
-    // 128 rows of 150,144: @@ us instead of @@.
+    // 128 rows of 150,144: 68.3 us instead of 72.5.
     auto gather = [&](const InBin &in, uint32_t n) {
       if (kHeld || t.size > 1 || few || use_k == use_p || in.hi == kInf) return false;
       sum_pieces(fmaxf(key_z(zkey(in.hi) + 1), zmin), [&](float4(&v)[kAhead], int e0) {

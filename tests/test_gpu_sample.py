@@ -190,6 +190,29 @@ def test_sample_strides_batches_and_repeats(V, stride):
     assert none is None and torch.equal(t3, token.cpu())
 
 
+@pytest.mark.parametrize("V", [9000, 150144])
+@pytest.mark.parametrize("k", [1, 20, 100, 256])
+def test_sample_few_of_uneven_rows(V, k):
+    """Top-k of up to 256 where the parts of a row are far apart: sorted both ways, all but one end
+    masked, one end far above, a single finite logit, more equal logits than a list holds."""
+    g = gen(V + k)
+    z = torch.empty(9, V).exponential_(generator=g)
+    z[1] = torch.sort(z[1]).values
+    z[2] = torch.sort(z[2], descending=True).values
+    z[3, V // 8:] = -math.inf
+    z[4, :V - 300] = -math.inf
+    z[5, :V // 9] += 100
+    z[6] = -math.inf
+    z[6, V - 1] = -5.0
+    z[7, :] = 1.0
+    z[8, 500:4500] = 30.0
+    u = torch.rand(9, generator=g)
+    B = 9
+    check(z, full(B, 0.9), full(B, k, torch.int32), full(B, 0.95), full(B, 0.0), u)
+    for b in range(9):
+        check(z[b:b + 1], full(1, 0.9), full(1, k, torch.int32), None, None, u[b:b + 1])
+
+
 @pytest.mark.parametrize("k,p,m", [(0, 0.9, 0.0), (0, 0.999, 1e-4), (400, 1.0, 0.0), (900, 0.8, 0.01),
                                    (30, 0.9, 0.0), (0, 1.0, 0.05)])
 @pytest.mark.parametrize("T", [0.2, 1.0])
