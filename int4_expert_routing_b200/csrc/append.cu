@@ -9,7 +9,7 @@
 // the half-split pairing, any two for the interleaved one.  So the rotation
 // needs no exchange, the norm one reduction over D / 16 lanes, and a lane's
 // eight angles are those of all heads and stay in registers.  16,384 tokens of
-// 32 + 4 heads of 128 (335 MB): 60 us, 5.6 TB/s, with two passes loaded ahead
+// 32 + 4 heads of 128 (335 MB): 60 us, 5.6 TB/s (5.4 with its launch, of 6.5 of a copy), with two passes loaded ahead
 // of the two at work; 68 without, 77 with five at once (fewer warps fit), 108
 // with blocks of tokens that wait for their angles.
 //
