@@ -321,28 +321,42 @@ def flint_int4_gemv_noalloc_status(stream=None) -> int:
 
 
 # ------------------------------------------------- the cache, its attention, sampling
+def _device() -> int:
+    """The current CUDA device."""
+    import torch
+    return torch._C._cuda_getDevice()
+
+
 def _local(where: str, *tensors, cache=None):
-    """The tensors' addresses.  Refuses tensors (the cache's among them) that
-    are not on the current CUDA device: the call launches there, and
-    ``stream`` is one of its streams."""
-    dev, ptrs = None, []
-    if cache is not None and cache._device is not None:
-        import torch
-        dev = cache._device
-        if dev != torch.cuda.current_device():
-            raise FlintError(FLINT_EINVAL, where)
+    """The tensors' device (None if all are raw addresses) and addresses.
+    Refuses tensors (the cache's among them) that are not on the current CUDA
+    device: the call launches there, and ``stream`` is one of its streams."""
+    dev, ptrs = None if cache is None else cache._device, []
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None:
+            ptrs.append(None)
+            continue
+        try:
+            on = t.get_device()
+        except AttributeError:  # an address
             ptrs.append(t)
             continue
-        on = t.get_device()
         if on != dev:
-            import torch
-            if on < 0 or dev is not None or on != torch.cuda.current_device():
+            if on < 0 or dev is not None:
                 raise FlintError(FLINT_EINVAL, where)
             dev = on
         ptrs.append(t.data_ptr())
-    return ptrs
+    if dev is not None and dev != _device():
+        raise FlintError(FLINT_EINVAL, where)
+    return dev, ptrs
+
+
+def _stream_on(dev, stream):
+    """``_stream`` where the current device is known."""
+    if stream is None and dev is not None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def make_kv_cache(k, v, k_scale=None, v_scale=None) -> flint_kv_cache:
@@ -378,11 +392,11 @@ def flint_kv_append(cache: flint_kv_cache, q, q_stride: int, k, k_stride: int, v
                     theta: float, q_norm, k_norm, q_out, q_out_stride: int, ws, ws_bytes: int,
                     stream=None):
     """``cache``: from ``make_kv_cache``."""
-    q, k, v, slots, pos, q_norm, k_norm, q_out, ws = _local(
+    dev, (q, k, v, slots, pos, q_norm, k_norm, q_out, ws) = _local(
         "flint_kv_append", q, k, v, slots, pos, q_norm, k_norm, q_out, ws, cache=cache)
     _check(lib().flint_kv_append(C.byref(cache), q, q_stride, k, k_stride, v, v_stride, T, q_heads,
                                  slots, pos, rope_dim, 1 if interleaved else 0, theta, q_norm,
-                                 k_norm, q_out, q_out_stride, ws, ws_bytes, _stream(stream)),
+                                 k_norm, q_out, q_out_stride, ws, ws_bytes, _stream_on(dev, stream)),
            "flint_kv_append")
 
 
@@ -391,17 +405,17 @@ def flint_attn_decode(cache: flint_kv_cache, q, q_stride: int, B: int, q_heads: 
                       window: int, sinks, out, out_stride: int, lse, ws, ws_bytes: int,
                       stream=None):
     """``cache``: from ``make_kv_cache``."""
-    q, page_table, lens, prefix_pages, sinks, out, lse, ws = _local(
+    dev, (q, page_table, lens, prefix_pages, sinks, out, lse, ws) = _local(
         "flint_attn_decode", q, page_table, lens, prefix_pages, sinks, out, lse, ws, cache=cache)
     _check(lib().flint_attn_decode(C.byref(cache), q, q_stride, B, q_heads, page_table, max_pages,
                                    lens, prefix_pages, prefix_len, scale, window, sinks, out,
-                                   out_stride, lse, ws, ws_bytes, _stream(stream)),
+                                   out_stride, lse, ws, ws_bytes, _stream_on(dev, stream)),
            "flint_attn_decode")
 
 
 def flint_sample(logits, stride: int, B: int, V: int, temperature, top_k, top_p, min_p, u, token,
                  logprob, stream=None):
-    logits, temperature, top_k, top_p, min_p, u, token, logprob = _local(
+    dev, (logits, temperature, top_k, top_p, min_p, u, token, logprob) = _local(
         "flint_sample", logits, temperature, top_k, top_p, min_p, u, token, logprob)
     _check(lib().flint_sample(logits, stride, B, V, temperature, top_k, top_p, min_p, u, token,
-                              logprob, _stream(stream)), "flint_sample")
+                              logprob, _stream_on(dev, stream)), "flint_sample")

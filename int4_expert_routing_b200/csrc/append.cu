@@ -211,13 +211,18 @@ __global__ void __launch_bounds__(kApThreads)
 cudaError_t launch_append(const AppendArgs &a, double theta, cudaStream_t st) {
   AppendKArgs p;
   p.a = a;
-  // theta^(-2i / rope_dim) from its powers at the bits of i: seven calls of pow
-  // instead of 64 (2 us), six roundings instead of one
+  // theta^(-2i / rope_dim) from its powers at the bits of i, and those as roots
+  // of the largest (a root halves an error): one call of pow instead of 64
+  // (2 us), six roundings instead of one
   p.freq[0] = 1.0 / 6.283185307179586476925;
-  for (int bit = 1; 2 * bit < a.rope_dim; bit *= 2) {
-    const double f = pow(theta, -2.0 * bit / a.rope_dim);
-    for (int i = bit; i < 2 * bit && i < 64; ++i) p.freq[i] = p.freq[i - bit] * f;
-  }
+  int top = 1;
+  while (4 * top < a.rope_dim) top *= 2;
+  double f[7];
+  f[6] = pow(theta, -2.0 * top / (a.rope_dim > 0 ? a.rope_dim : 1));
+  int at = 6;
+  for (int bit = top; bit > 1; bit /= 2, --at) f[at - 1] = sqrt(f[at]);
+  for (int bit = 1; bit <= top; bit *= 2, ++at)
+    for (int i = bit; i < 2 * bit; ++i) p.freq[i] = p.freq[i - bit] * f[at];
   // A token's heads go to one warp, or in a call of few tokens to several, one
   // pass each at the least.
   const int per_pass = 512 / a.head_dim, heads = a.q_heads + 2 * a.heads;

@@ -147,15 +147,10 @@ def test_theta_below_one_and_tables_too_large():
     refused(attend, B=F.MAX_ATTN_B, max_pages=1 << 20, prefix_len=20)
 
 
-def test_binding_refuses_a_cache_of_another_device():
+def test_binding_refuses_a_cache_of_another_device(monkeypatch):
     """The cache's tensors are on device 1, the call's (raw addresses) wherever the current one is."""
-    torch = pytest.importorskip("torch")
     c = cache()
     c._device = 1
-    current = torch.cuda.current_device
-    torch.cuda.current_device = lambda: 0
-    try:
-        refused(append, c)
-        refused(attend, c)
-    finally:
-        torch.cuda.current_device = current
+    monkeypatch.setattr(F, "_device", lambda: 0)
+    refused(append, c)
+    refused(attend, c)
