@@ -213,9 +213,16 @@ struct AtJoin {
   static constexpr int kCopy = 8 * kNT * kPitch, kFloats = kCopies * kCopy;
 };
 
+// CTAs of an SM: 16 rows of 128 elements leave no registers for the third (at
+// 128 a thread 1,200 bytes spilled).
+template <int kD, bool kF8, int kNT>
+struct AtCtas {
+  static constexpr int kCtas = kD == 128 && kNT == 2 ? 2 : AtTile<kD, kF8>::kCtas;
+};
+
 // kRows = 8 kNT query rows a unit
 template <int kD, bool kF8, int kNT, bool kPre>
-__global__ void __launch_bounds__(kAtThreads, AtTile<kD, kF8>::kCtas)
+__global__ void __launch_bounds__(kAtThreads, (AtCtas<kD, kF8, kNT>::kCtas))
     k_attn_parts(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ AttnK a) {
   using Tile = AtTile<kD, kF8>;
@@ -582,18 +589,33 @@ __global__ void __launch_bounds__(kAtThreads, AtTile<kD, kF8>::kCtas)
         for (int x = 0; x < kAtWarps / Join::kCopies; ++x) {
           if (warp / Join::kCopies == x) {
             float *mine = osum + warp % Join::kCopies * Join::kCopy;
+            auto at = [&](int k, int nt, int i) {
+              const int r = 8 * nt + 2 * t4 + (i & 1);
+              const int e = kF8 ? 16 * k + 2 * g + (i >> 1) : 16 * k + g + 8 * (i >> 1);
+              return &mine[r * Join::kPitch + e];
+            };
+            // eight loads under way, then their stores: the compiler does not
+            // move a load over a store (40 sequences of 100 to 9,000 keys, 16
+            // query heads on one: 22 us, one by one 42)
+            constexpr int kBatch = 2 / kNT;
 #pragma unroll
-            for (int k = 0; k < kKs; ++k)
+            for (int k0 = 0; k0 < kKs; k0 += kBatch) {
+              float old[kBatch][kNT][4];
 #pragma unroll
-              for (int nt = 0; nt < kNT; ++nt)
+              for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int r = 8 * nt + 2 * t4 + (i & 1);
-                  const int e = kF8 ? 16 * k + 2 * g + (i >> 1) : 16 * k + g + 8 * (i >> 1);
-                  const float v = o[k][nt][i] * fac[nt][i & 1];
-                  float *dst = &mine[r * Join::kPitch + e];
-                  *dst = x == 0 ? v : *dst + v;
-                }
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    old[k][nt][i] = x == 0 ? 0.f : *at(k0 + k, nt, i);
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    *at(k0 + k, nt, i) = fmaf(o[k0 + k][nt][i], fac[nt][i & 1], old[k][nt][i]);
+            }
           }
           asm volatile("bar.sync 1, 128;" ::: "memory");
         }
@@ -848,15 +870,19 @@ cudaError_t launch_attn_as(const flint_kv_cache &c, const CUtensorMap &k, const 
                            AttnK &a, int sms, cudaStream_t st) {
   cudaError_t e;
   const int rows = a.B * a.G;
-  constexpr int kCtas = AtTile<kD, kF8>::kCtas;
-  const int wide = kCtas * sms < kAtMaxCtas ? kCtas * sms : kAtMaxCtas;
+  auto wide_of = [&](bool two) {
+    const int ctas = two ? AtCtas<kD, kF8, 2>::kCtas : AtCtas<kD, kF8, 1>::kCtas;
+    return ctas * sms < kAtMaxCtas ? ctas * sms : kAtMaxCtas;
+  };
+  const int wide = wide_of(a.G > 8);
   a.behind_prefix = a.prefix_len > 0 && a.window == 0;
   if (a.behind_prefix) {
     if (a.pre_rows <= kAtSmallRows) {
       const long long tiles = (long long)ceil_div(rows, a.pre_rows) * a.H *
                               ceil_div(a.prefix_len, kAtKeys);
       a.pre_keys = kAtKeys, a.pre_visit = 0;
-      a.ctas_pre = (int)(tiles < wide ? tiles : wide);
+      const int wide_pre = wide_of(a.pre_rows > 8);
+      a.ctas_pre = (int)(tiles < wide_pre ? tiles : wide_pre);
       note_step("attention prefix launch");
       e = a.pre_rows == 8 ? launch_parts<kD, kF8, 1, true>(k, v, a, a.ctas_pre, st)
                           : launch_parts<kD, kF8, 2, true>(k, v, a, a.ctas_pre, st);
